@@ -41,10 +41,26 @@ class WcShape(ctypes.Structure):
     ]
 
 
+class WcCache(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("dv", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("k_page", ctypes.c_int64), ("k_head", ctypes.c_int64), ("k_token", ctypes.c_int64),
+        ("v_page", ctypes.c_int64), ("v_head", ctypes.c_int64), ("v_token", ctypes.c_int64),
+    ]
+
+
+class WcRowStrides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
 EXPORTS = [
     "wc_f_ld", "wc_workspace_bytes", "wc_forward_workspace_bytes", "wc_select", "wc_weights", "wc_attend",
     "wc_forward", "wc_check_device_status", "wc_selftest_wait_timeout", "wc_status_string",
-    "wc_attend_noalloc", "wc_selftest_exp2", "wc_read_bandwidth_probe",
+    "wc_attend_noalloc", "wc_selftest_exp2", "wc_read_bandwidth_probe", "wc_cache_workspace_bytes",
+    "wc_cache_append", "wc_cache_attend", "wc_cache_evict",
 ]
 
 _lib = None
@@ -88,6 +104,14 @@ def lib():
         L.wc_selftest_exp2.restype = i32
         L.wc_read_bandwidth_probe.argtypes = [vp, ctypes.c_int64, vp, vp]
         L.wc_read_bandwidth_probe.restype = i32
+        cp, rp, i64, c32 = ctypes.POINTER(WcCache), ctypes.POINTER(WcRowStrides), ctypes.c_int64, ctypes.c_int32
+        L.wc_cache_workspace_bytes.argtypes, L.wc_cache_workspace_bytes.restype = [cp, c32], sz
+        L.wc_cache_append.argtypes = [cp, c32, vp, rp, vp, rp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.wc_cache_append.restype = i32
+        L.wc_cache_attend.argtypes = [cp, vp, i64, i64, vp, vp, vp, vp, c32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.wc_cache_attend.restype = i32
+        L.wc_cache_evict.argtypes = [cp, c32, c32, c32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.wc_cache_evict.restype = i32
         _lib = L
     return _lib
 
@@ -331,6 +355,204 @@ class HostPipeline:
     def wait(self):
         self.compute.synchronize()
         return check_device_status(self.ws, self.compute)
+
+
+def _strides(t):
+    """Strides of a 4-axis tensor's first three axes, 0 where the axis has one entry."""
+    return [st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3])]
+
+
+class PagedCache:
+    """Exact keys and values in pages, beside (or instead of) a coreset: rows
+    appended as tokens are generated, attention of one new token per sequence
+    over them, eviction by accumulated attention weight.
+
+    k_pages [n_pages, Hkv, page, d] and v_pages [n_pages, Hkv, page, dv] are
+    CUDA tensors (bf16 or fp32) with contiguous rows; a pool kept in the order
+    [n_pages, page, Hkv, d] is passed as its transpose(1, 2).  table
+    [B, max_pages] int32 (contiguous): token t of sequence b is in slot
+    t % page of page table[b, t // page].  hq: query heads.  scores
+    [B, Hkv, max_pages * page] fp32 (contiguous): accumulated attention
+    weights, needed to accumulate and to evict.
+
+    Lengths, positions and counts are int32 CUDA tensors that the caller keeps
+    and advances, so a captured graph serves a growing cache.  The tensors
+    given here are kept by reference and changed in place.  Lengths and page
+    numbers are checked on the device (`check()` reports).  The cache's calls
+    share one workspace: calls that may overlap on the GPU (two streams, two
+    graphs replayed at once) need a PagedCache each.
+
+        cache = wildcat.PagedCache(k_pages, v_pages, table, hq=32, scores=scores)
+        cache.append(K, V, lens); lens += 1                   # K, V [B, Hkv, 1, d]
+        out = cache.attend(Q, lens, accumulate=True)          # Q [B, Hq, d]
+        lens = cache.evict(lens, keep=1024, sink=4, recent=64)["lens"]
+        out = cache.attend(Q, lens, coreset=(Ks, W, rank))    # a compressed prompt and the exact tail
+    """
+
+    def __init__(self, k_pages, v_pages, table, hq, *, scores=None, scale=0.0):
+        if k_pages.dim() != 4 or v_pages.dim() != 4 or table.dim() != 2:
+            raise WildcatError(1, "PagedCache: k_pages and v_pages have 4 axes, table 2")
+        self.device = k_pages.device
+        n_pages, hkv, page, d = k_pages.shape
+        self.dtype = k_pages.dtype
+        if self.dtype not in (torch.float32, torch.bfloat16) or v_pages.dtype != self.dtype:
+            raise WildcatError(1, "PagedCache: k_pages and v_pages are both bf16 or both fp32")
+        if tuple(v_pages.shape[:3]) != (n_pages, hkv, page):
+            raise WildcatError(1, "PagedCache: v_pages differs from k_pages in more than its width")
+        if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+            raise WildcatError(1, "PagedCache: rows of k_pages and v_pages are contiguous")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.batch, self.max_pages = table.shape
+        self.hkv, self.d, self.dv, self.hq = hkv, d, v_pages.shape[3], int(hq)
+        self.cap = self.max_pages * page
+        self.table = self._tensor(table, "table", (self.batch, self.max_pages), torch.int32)
+        self.scores = None if scores is None else self._scores(scores, "scores")
+        self._on_device(v_pages, "v_pages")
+        self.shape = WcCache(self.batch, self.hq, hkv, d, self.dv,
+                             WC_BF16 if self.dtype == torch.bfloat16 else WC_F32, page, n_pages, self.max_pages,
+                             scale, *_strides(k_pages), *_strides(v_pages))
+        n = int(lib().wc_cache_workspace_bytes(ctypes.byref(self.shape), int(scores is not None)))
+        if n == 0:
+            raise WildcatError(1, "PagedCache: sizes or strides")
+        if self.device.type != "cuda":
+            raise WildcatError(1, "PagedCache: the pages are on a GPU")
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+
+    # ---- arguments
+
+    def _on_device(self, t, name):
+        if t.device != self.device:
+            raise WildcatError(1, f"PagedCache: {name} is on {t.device}, the pages on {self.device}")
+
+    def _tensor(self, t, name, shape, dtype):
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+            raise WildcatError(1, f"PagedCache: {name} is a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                                  f"{t.dtype} {tuple(t.shape)}")
+        self._on_device(t, name)
+        return t
+
+    def _scores(self, t, name):
+        return self._tensor(t, name, (self.batch, self.hkv, self.cap), torch.float32)
+
+    def _rows(self, t, name, shape):
+        """A strided tensor of rows in the pages' type."""
+        if tuple(t.shape) != tuple(shape) or t.dtype != self.dtype:
+            raise WildcatError(1, f"PagedCache: {name} is a {self.dtype} tensor of shape {tuple(shape)}, got "
+                                  f"{t.dtype} {tuple(t.shape)}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise WildcatError(1, f"PagedCache: rows of {name} are contiguous")
+        self._on_device(t, name)
+        return t
+
+    def _launch(self, stream, call, what, tensors):
+        """`call(stream handle)` on the given stream, or the device's current
+        one.  The caching allocator is told of the tensors' use on a given one."""
+        current = torch.cuda.current_stream(self.device)
+        s = current if stream is None else stream
+        if s.device != self.device:
+            raise WildcatError(1, f"{what}: the stream is another device's")
+        if s != current:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+        with torch.cuda.device(self.device):
+            _check(call(ctypes.c_void_p(s.cuda_stream)), what)
+
+    # ---- calls
+
+    def append(self, K, V, pos, count=None, *, stream=None):
+        """Writes row j < count[b] (count None: every row) of K [B, Hkv, t, d]
+        and V [B, Hkv, t, dv] to position pos[b] + j of sequence b; the scores
+        there become 0.  pos, count: int32 [B].  K and V may be strided in
+        steps of 16 bytes.  Rows beyond the cache's end are not written and
+        reported by `check()`."""
+        t = K.shape[2] if K.dim() == 4 else -1
+        K = self._rows(K, "K", (self.batch, self.hkv, t, self.d))
+        V = self._rows(V, "V", (self.batch, self.hkv, t, self.dv))
+        pos = self._tensor(pos, "pos", (self.batch,), torch.int32)
+        if count is not None:
+            count = self._tensor(count, "count", (self.batch,), torch.int32)
+        ws, ks, vs = self.ws, WcRowStrides(*_strides(K)), WcRowStrides(*_strides(V))
+        self._launch(stream, lambda s: lib().wc_cache_append(
+            ctypes.byref(self.shape), t, _ptr(K), ctypes.byref(ks), _ptr(V), ctypes.byref(vs), _ptr(pos),
+            _ptr(count), _ptr(self.k_pages), _ptr(self.v_pages), _ptr(self.table), _ptr(self.scores), _ptr(ws),
+            ws.numel(), s), "wc_cache_append", (K, V, pos, count, self.k_pages, self.v_pages, self.table,
+                                                self.scores, ws))
+
+    def attend(self, Q, lens, *, coreset=None, accumulate=False, return_lse=False, out=None, stream=None):
+        """Attention of one new token per sequence: Q [B, Hq, d] over the first
+        lens[b] tokens of sequence b, and over coreset = (Ks, W, rank) beside
+        them (as `weights` and `select` return them; rank None: all r rows).
+        Returns out [B, Hq, dv] fp32, or (out, lse [B, Hq]).  accumulate: adds
+        each key's attention weight, summed over its queries, to `scores`."""
+        Q = self._rows(Q, "Q", (self.batch, self.hq, self.d))
+        lens = self._tensor(lens, "lens", (self.batch,), torch.int32)
+        if accumulate and self.scores is None:
+            raise WildcatError(1, "PagedCache.attend: accumulate needs scores")
+        Ks = W = rank = None
+        r = 0
+        if coreset is not None:
+            Ks, W, rank = coreset
+            r = Ks.shape[2] if Ks.dim() == 4 else -1
+            Ks = self._tensor(Ks, "Ks", (self.batch, self.hkv, r, self.d), self.dtype)
+            W = self._tensor(W, "W", (self.batch, self.hkv, r, self.dv + 1), torch.float32)
+            if rank is not None:
+                rank = self._tensor(rank, "rank", (self.batch, self.hkv), torch.int32)
+        ws = self.ws
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty(self.batch, self.hq, self.dv, dtype=torch.float32, device=self.device)
+            else:
+                out = self._tensor(out, "out", (self.batch, self.hq, self.dv), torch.float32)
+            lse = torch.empty(self.batch, self.hq, dtype=torch.float32, device=self.device) if return_lse else None
+        scores = self.scores if accumulate else None
+        self._launch(stream, lambda s: lib().wc_cache_attend(
+            ctypes.byref(self.shape), _ptr(Q), Q.stride(0), Q.stride(1), _ptr(self.k_pages), _ptr(self.v_pages),
+            _ptr(self.table), _ptr(lens), r, _ptr(Ks), _ptr(W), _ptr(rank), _ptr(out), _ptr(lse), _ptr(scores),
+            _ptr(ws), ws.numel(), s), "wc_cache_attend",
+            (Q, lens, Ks, W, rank, out, scores, self.k_pages, self.v_pages, self.table, ws))
+        return (out, lse) if return_lse else out
+
+    def evict(self, lens, keep, *, sink=0, recent=0, into=None, scores_into=None, lens_out=None, stream=None):
+        """Shortens every sequence to at most `keep` tokens, each kv head by
+        itself: the first `sink`, the last `recent` and those of the largest
+        scores in between (ties: the lower position).  The kept rows move, in
+        order, to the front of the sequence's pages, or to the pages of `into`
+        (a table like `table`, which is not changed; needed where pages are
+        shared), their scores to the front of `scores`, or of `scores_into`.
+        Returns idx [B, Hkv, keep] (kept positions, -1 beyond) and lens [B]
+        (lens_out may be lens itself).  A sequence that cannot be moved (a page
+        outside the pool, a page to be written that is named twice) stays as it
+        is; `check()` reports it."""
+        lens = self._tensor(lens, "lens", (self.batch,), torch.int32)
+        if self.scores is None:
+            raise WildcatError(1, "PagedCache.evict: needs scores")
+        if into is not None:
+            into = self._tensor(into, "into", (self.batch, self.max_pages), torch.int32)
+        if scores_into is not None:
+            scores_into = self._scores(scores_into, "scores_into")
+        keep, sink, recent = int(keep), int(sink), int(recent)
+        if not (1 <= keep <= self.cap and sink >= 0 and recent >= 0 and sink + recent <= keep):
+            raise WildcatError(1, "PagedCache.evict: 1 <= keep <= capacity, sink + recent <= keep")
+        ws = self.ws
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            idx = torch.empty(self.batch, self.hkv, keep, dtype=torch.int32, device=self.device)
+            if lens_out is None:
+                lens_out = torch.empty(self.batch, dtype=torch.int32, device=self.device)
+            else:
+                lens_out = self._tensor(lens_out, "lens_out", (self.batch,), torch.int32)
+        self._launch(stream, lambda s: lib().wc_cache_evict(
+            ctypes.byref(self.shape), keep, sink, recent, _ptr(self.k_pages), _ptr(self.v_pages), _ptr(self.table),
+            _ptr(into), _ptr(lens), _ptr(self.scores), _ptr(scores_into), _ptr(idx), _ptr(lens_out), _ptr(ws),
+            ws.numel(), s), "wc_cache_evict",
+            (lens, into, scores_into, lens_out, self.scores, self.k_pages, self.v_pages, self.table, ws))
+        return dict(idx=idx, lens=lens_out)
+
+    def check(self, stream=None) -> int:
+        """The first error the cache's kernels recorded since the last check
+        (0: none), after waiting for the stream; clears it."""
+        with torch.cuda.device(self.device):
+            return check_device_status(self.ws, stream)
 
 
 def check_device_status(ws, stream=None) -> int:

@@ -92,7 +92,9 @@ typedef enum {
     WC_ERR_NUMERIC = 6,      /* non-finite value met on the device */
     WC_ERR_BOUNDS = 7        /* an index outside its buffer (pivot, rank), recorded by the
                                 bounds-checked debug build (libwildcat_debug.so), which
-                                skips the access instead of faulting */
+                                skips the access instead of faulting.  The paged cache's
+                                calls check lengths, positions and page numbers in every
+                                build and record it too */
 } wc_status;
 
 typedef enum { WC_F32 = 0, WC_BF16 = 1 } wc_dtype;
@@ -260,6 +262,109 @@ wc_status wc_read_bandwidth_probe(const void* buf, int64_t bytes, uint32_t* sink
  */
 wc_status wc_attend_noalloc(const wc_shape* shape, const void* Q, const void* Ks, const float* W,
                             const int32_t* rank, float* out, void* stream);
+
+/*
+ * Paged key-value cache: the exact keys and values of tokens that are not (or
+ * not yet) compressed into a coreset, kept in pages; attention of one new
+ * token per sequence over them; eviction by accumulated attention weight.
+ *   - Pools: k [n_pages, Hkv, page, d], v [n_pages, Hkv, page, dv], dtype, rows
+ *     contiguous, the other strides free (below), so a pool in the order
+ *     [n_pages, page, Hkv, d] is the same call with other strides.
+ *   - table [B, max_pages] int32: token t of sequence b is in slot t % page of
+ *     page table[b, t / page].  Entries of pages that no token uses are not
+ *     read.  A sequence holds up to cap = max_pages * page tokens.
+ *   - Lengths, positions and counts are int32 device arrays, so a captured
+ *     graph serves a growing cache.  Every build checks them and the page
+ *     numbers on the device: a length outside [0, cap] is held to that range,
+ *     keys in a page whose number is outside [0, n_pages) are left out of the
+ *     attention, a row that would go outside the cache or to such a page is
+ *     not written; each records WC_ERR_BOUNDS (wc_check_device_status).
+ *   - scores [B, Hkv, cap] fp32: attention weight accumulated by position.
+ *     They belong to a sequence, not to a page.
+ *   - The workspace is the cache calls' own layout (wc_cache_workspace_bytes),
+ *     256-byte aligned, its first 4 bytes zero before the first call.  Calls
+ *     that may overlap (two streams, two graphs) need a workspace each.
+ */
+typedef struct {
+    int32_t batch;      /* B sequences, 1..65535 */
+    int32_t hq;         /* query heads, a multiple of hkv, B * hq <= 2^24 */
+    int32_t hkv;        /* key/value heads, 1..65535 */
+    int32_t d;          /* key width, a multiple of 8, 8..256 */
+    int32_t dv;         /* value width, a multiple of 8, 8..256 */
+    int32_t dtype;      /* wc_dtype of the pools, Q and Ks */
+    int32_t page;       /* tokens per page, 1..65536 */
+    int32_t n_pages;    /* pages in the pools */
+    int32_t max_pages;  /* table entries per sequence; max_pages * page <= 2^30 */
+    float scale;        /* beta; 0 selects 1/sqrt(d) */
+    int64_t k_page, k_head, k_token;  /* strides of k in elements, multiples of 16 bytes, each */
+    int64_t v_page, v_head, v_token;  /* at least a row where its axis is longer than 1; all
+                                         six 0: dense pools in the order above */
+} wc_cache;
+
+/* Workspace bytes of every cache call, with accumulation (1) or without (0);
+ * 0 if the cache is invalid.  Accumulation keeps the step's logits, 4 B Hq cap
+ * bytes. */
+size_t wc_cache_workspace_bytes(const wc_cache* cache, int32_t accumulate);
+
+/*
+ * cache_append — new rows K [B, Hkv, t, d], V [B, Hkv, t, dv] (rows contiguous,
+ * 16-byte aligned; strides in elements, multiples of 16 bytes) into the pages:
+ * row j < count[b] goes to position pos[b] + j (count NULL: all t rows), and
+ * scores (if not NULL) become 0 at the positions written.  Nothing else
+ * changes; the lengths are the caller's to advance.  Two rows sent to one
+ * place leave one of them.
+ */
+typedef struct { int64_t batch, head, row; } wc_row_strides;
+wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const wc_row_strides* k_strides,
+                          const void* V, const wc_row_strides* v_strides, const int32_t* pos,
+                          const int32_t* count, void* k, void* v, const int32_t* table, float* scores,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * cache_attend — attention of one new token per sequence: Q [B, Hq, d] (rows
+ * contiguous, strides in elements) over the first lens[b] tokens of each
+ * sequence, and over a coreset where one is given (r > 0: Ks [B, Hkv, r, d],
+ * W [B, Hkv, r, dv+1] fp32 and rank [B, Hkv] as wc_weights leaves them, rank
+ * NULL: all r rows): one softmax over both,
+ *   a_i = exp(beta <q, k_i>)  for i < lens[b],   a'_s = exp(beta <q, ks_s>)
+ *   L = sum_i a_i + sum_s a'_s W[s, dv]
+ *   out[b, g, :] = (sum_i a_i v_i + sum_s a'_s W[s, :dv]) / L,  lse[b, g] = log L
+ * out [B, Hq, dv] fp32, lse [B, Hq] fp32 or NULL.  A sequence without tokens
+ * (and without coreset rows) gets out = 0, lse = -inf.  With scores (not NULL)
+ *   scores[b, h, i] += sum over the queries g of kv head h of a_i / L,
+ * positions from lens[b] on left as they were.  The sums are split over the
+ * blocks of the launch and joined in a fixed order: results repeat bit for bit
+ * for the same lengths, shape and GPU.
+ */
+wc_status wc_cache_attend(const wc_cache* cache, const void* Q, int64_t q_batch, int64_t q_head, const void* k,
+                          const void* v, const int32_t* table, const int32_t* lens, int32_t r, const void* Ks,
+                          const float* W, const int32_t* rank, float* out, float* lse, float* scores,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * cache_evict — shortens every sequence to at most `keep` tokens by the
+ * accumulated scores, for each kv head by itself.  A sequence with lens[b] >
+ * keep keeps its first `sink` and last `recent` tokens (sink + recent <= keep)
+ * and, of the others, the keep - sink - recent with the largest scores (equal
+ * scores: the lower position first; a NaN counts as -inf; -0 equals 0).  The
+ * kept tokens move, in order of position, to positions 0 .. keep-1 of `into`
+ * (a table like `table`; NULL: the sequence's own pages), their scores to
+ * scores_into (NULL: scores itself).  Shorter sequences keep every token (and
+ * are copied where `into` or scores_into is given).
+ *   idx [B, Hkv, keep]  the kept positions in ascending order, -1 beyond
+ *   lens_out [B]        min(lens[b], keep); may be lens itself
+ * Rows and scores behind the new length are left as they were.  scores_into
+ * is scores or does not overlap it.
+ * A sequence is refused as a whole (idx -1, lens_out = lens[b], its pages and
+ * scores unchanged) and the reason recorded, when one of its pages is outside
+ * the pool (WC_ERR_BOUNDS), or when a page that would be written is named
+ * twice: by two sequences, twice by one, or as one of `into` and of `table`
+ * (WC_ERR_INVALID).  Pages that are only read may be shared.
+ */
+wc_status wc_cache_evict(const wc_cache* cache, int32_t keep, int32_t sink, int32_t recent, void* k, void* v,
+                         const int32_t* table, const int32_t* into, const int32_t* lens, const float* scores,
+                         float* scores_into, int32_t* idx, int32_t* lens_out, void* ws, size_t ws_bytes,
+                         void* stream);
 
 /* Static text for a status code. */
 const char* wc_status_string(wc_status status);
