@@ -53,7 +53,10 @@ wc_status make_view(const wc_cache* in, View* o) {
 }
 
 // Query rows of one unit of the attention's work.
-static int rows_of(const View& s) { return s.group >= 5 ? 8 : s.group >= 3 ? 4 : s.group; }
+static int rows_of(const View& s) {
+    if (s.dtype == WC_BF16) return s.group > 8 ? 16 : s.group > 4 ? 8 : 4;
+    return s.group >= 5 ? 8 : s.group >= 3 ? 4 : s.group;
+}
 
 // Coreset rows of one block: whole 64-row steps, about kCoresetBlocks blocks over all units (at
 // most units + kCoresetBlocks, which the workspace holds).

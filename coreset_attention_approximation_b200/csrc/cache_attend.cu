@@ -8,6 +8,9 @@
 // The key tiles of the whole batch are divided evenly over the blocks
 // (wc_cache.cuh), whatever the lengths, and a second kernel joins a unit's
 // partial rows in order of the blocks.
+#include <atomic>
+#include <mutex>
+
 #include "wc_cache.cuh"
 
 namespace wc {
@@ -56,16 +59,6 @@ template <> __device__ __forceinline__ void load_chunk<__nv_bfloat16>(const char
         x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
 }
-// Four consecutive values as floats.
-__device__ __forceinline__ void load_four(const char* row, int chunk, float x[4], float) {
-    load_chunk<float>(row + chunk * 16, x);
-}
-__device__ __forceinline__ void load_four(const char* row, int chunk, float x[4], __nv_bfloat16) {
-    const uint2 v = *reinterpret_cast<const uint2*>(row + chunk * 8);
-    x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xffff0000u);
-    x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-
 // The running state of one warp: its keys' sums for RG query rows.
 template <int RG, int NVI>
 struct Running {
@@ -320,14 +313,16 @@ __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
     join_warps<RG>(a, merge, a.cparts + (int64_t)index * a.rows * c1_row(s.dv), 0, rows);
 }
 
-// The pages' share on CUDA cores, any type and width.  Each warp takes NT keys
+// fp32 pages, on CUDA cores (their products keep 24 bits).  Each warp takes NT keys
 // of every 4 NT-key tile through its own two stages of shared memory (filled
 // by cp.async, so warps never wait for one another inside a unit); a lane
 // holds one key's logits for the RG query rows, then four value columns.
-template <typename T, int RG, int NT, int NVI>
+template <int RG, int NT, int NVI>
 __global__ void __launch_bounds__(kThreads) cache_attend_simt_kernel(const AttendArgs a) {
-    extern __shared__ __align__(16) char smem[];
+    using T = float;
+    extern __shared__ __align__(128) char smem[];
     __shared__ int64_t place_sh[4 + kWarps];
+    grid_dependents_launch();
     const View& s = a.s;
     const int blocks = a.blocks;
     if ((int)blockIdx.x >= blocks) {
@@ -372,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) cache_attend_simt_kernel(const Atten
             const int key = i * kTile + warp * NT + lane;
             if (lane < NT && i < k1 && key < len) {
                 const int tp = key / s.page, slot = key - tp * s.page;
-                const int pg = checked_page(s, a.s.table, b, tp, a.status);
+                const int pg = checked_page(s, s.table, b, tp, a.status);
                 if (pg >= 0) {
                     w.k = pg * s.k_page + slot * s.k_token;
                     w.v = pg * s.v_page + slot * s.v_token;
@@ -435,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) cache_attend_simt_kernel(const Atten
                     const int ch = lane % cols + n * cols;
                     if (ch < vchunks) {
                         float y[4];
-                        load_four(vrows + j * L.v_row, ch, y, T());
+                        load_chunk<float>(vrows + j * L.v_row + ch * 16, y);
 #pragma unroll
                         for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -452,6 +447,373 @@ __global__ void __launch_bounds__(kThreads) cache_attend_simt_kernel(const Atten
         const int64_t unit = (int64_t)b * per_tile + in_b;
         join_warps<RG>(a, merge, whole ? nullptr : a.parts + (unit + c) * a.rows * c1_row(s.dv),
                        (int64_t)b * s.hq + g0, rows);
+        __syncthreads();
+        t += k1 - k0;
+        k0 = 0;
+        if (t < t_last && ++in_b == per_tile) {
+            in_b = 0;
+            do {
+                len = checked_len(a.lens, ++b, s.cap, a.status);
+            } while (len == 0);
+            tiles = (len + kTile - 1) / kTile;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- tensor cores
+
+__device__ __forceinline__ void ldmatrix4(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// a b, 16 x 8 x 16, bf16 in, fp32 sums.
+__device__ __forceinline__ void mma16816_new(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// c += a b.
+__device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The three bf16 terms of a pair of weights, x = t0 + t1 + t2 up to 2^-24 x:
+// one term alone (half a step, 2^-9 relative) would be the largest error of the
+// whole attention, whose output is fp32.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t t[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        t[i] = pack_bf16(x, y);
+        x -= __uint_as_float(t[i] << 16);
+        y -= __uint_as_float(t[i] & 0xffff0000u);
+    }
+}
+
+constexpr int kMmaKeys = 16;     // keys of one warp's step
+constexpr int kMmaStages = 3;
+
+// bf16 pages on tensor cores (mma.sync: a group's 1 to 16 query rows fill one
+// 16-row tile at most, and the pass is bound by the bytes of the keys and
+// values, so the wider tcgen05 tiles would only hold more padding).  A warp
+// takes 16 keys of every 64-key tile through its own ring of three stages;
+// 128-byte groups of a row are XOR-swizzled by the row so that ldmatrix reads
+// without bank conflicts.  DP: d and dv rounded up to 64, 128 or 256 (columns
+// past the width are zeros).
+// SETS: how the weights' three terms meet the 16 rows of the value product.
+//   1  up to 4 query rows, each four times in the tile (r, r + 4, r + 8, r + 12):
+//      the copies carry the terms, so one product adds all three
+//   2  up to 8 rows, each twice: two products
+//   3  up to 16 rows: three products
+template <int DP, int SETS>
+__global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const AttendArgs a) {
+    using bf16 = __nv_bfloat16;
+    constexpr int kRows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
+    constexpr int kChunks = DP / 8;                        // 16-byte pieces of a row
+    constexpr int kRowBytes = DP * 2;
+    constexpr int kStage = 2 * kMmaKeys * kRowBytes;       // keys, then values
+    constexpr int kTile = kWarps * kMmaKeys;
+    constexpr int kPerLoad = 32 / kChunks > 0 ? 32 / kChunks : 1;   // rows of one warp-wide load
+    constexpr int kLoads = kMmaKeys * kChunks / 32;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ int64_t place_sh[4 + kWarps];
+    grid_dependents_launch();
+    const View& s = a.s;
+    const int blocks = a.blocks;
+    if ((int)blockIdx.x >= blocks) {
+        coreset_block<bf16, kRows, 16>(a, blockIdx.x - blocks, smem);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = lane >> 2, pair = lane & 3;           // fragment row and column pair
+    char* stages = smem + warp * kMmaStages * kStage;
+    const uint32_t stages_u = (uint32_t)__cvta_generic_to_shared(stages);
+    const int per_tile = s.hkv * a.row_tiles;
+    const int c = blockIdx.x;
+    const Place at = find_place<kThreads>(s, a.lens, kTile, per_tile, c, blocks, -1, a.status, place_sh);
+    if (c >= at.blocks) return;
+    int64_t t = block_first(at.total, c, at.blocks);
+    const int64_t t_last = block_first(at.total, c + 1, at.blocks);
+    int b = at.b;
+    int len = checked_len(a.lens, b, s.cap, a.status);
+    int tiles = (len + kTile - 1) / kTile;
+    int in_b = (int)((t - at.before) / tiles);
+    int k0 = (int)((t - at.before) % tiles);
+    const int ck = s.d / 8, cv = s.dv / 8;
+    const bool whole_pages = s.page % kMmaKeys == 0;       // 16 keys of a step then share a page
+    while (t < t_last) {
+        const int k1 = (int)min((int64_t)tiles, k0 + (t_last - t));
+        const int h = in_b / a.row_tiles, rt = in_b % a.row_tiles;
+        const int rows = min(a.rows, s.group - rt * a.rows), g0 = h * s.group + rt * a.rows;
+        const char* kh = a.kp + h * s.k_head;
+        const char* vh = a.vp + h * s.v_head;
+        // Query fragments, as they are (the logits are scaled in fp32): rows
+        // quad and, where the rows are not copies, quad + 8.
+        uint32_t q[DP / 16][SETS == 3 ? 4 : 2];
+        {
+            const bf16* src = static_cast<const bf16*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
+            auto two = [&](int row, int col) {
+                uint32_t v = 0;
+                if (row < rows && col < s.d) {
+                    const bf16* p = src + row * a.q_head + col;
+                    v = (uint32_t)__bfloat16_as_ushort(p[0]) | (uint32_t)__bfloat16_as_ushort(p[1]) << 16;
+                }
+                return v;
+            };
+            const int r0 = quad % kRows;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                const int col = k * 16 + pair * 2;
+                if (SETS == 3) {
+                    q[k][0] = two(quad, col); q[k][1] = two(quad + 8, col);
+                    q[k][SETS == 3 ? 2 : 0] = two(quad, col + 8); q[k][SETS == 3 ? 3 : 1] = two(quad + 8, col + 8);
+                } else {
+                    q[k][0] = two(r0, col);
+                    q[k][1] = two(r0, col + 8);
+                }
+            }
+        }
+        float o[DP / 8][4];
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+        constexpr int kMine = SETS == 3 ? 2 : 1;           // rows of this lane
+        float m[kMine], l[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
+
+        // lane j < 16: where key j of tile i is, and how many keys there are
+        auto locate = [&](int i) {
+            KeyPlace w{0, 0, false};
+            const int key = i * kTile + warp * kMmaKeys + (whole_pages ? 0 : lane & 15);
+            if (i < k1 && key < len) {
+                const int tp = key / s.page, slot = key - tp * s.page;
+                const int pg = checked_page(s, s.table, b, tp, a.status);
+                if (pg >= 0) {
+                    w.k = pg * s.k_page + slot * s.k_token;
+                    w.v = pg * s.v_page + slot * s.v_token;
+                    w.valid = true;
+                }
+            }
+            return w;
+        };
+        auto live_keys = [&](int i, const KeyPlace& w) {
+            const int n = len - (i * kTile + warp * kMmaKeys);
+            if (i >= k1 || n <= 0) return 0u;
+            if (!whole_pages) return __ballot_sync(0xffffffffu, w.valid) & 0xffffu;
+            return w.valid ? (n >= kMmaKeys ? 0xffffu : (1u << n) - 1) : 0u;
+        };
+        auto load = [&](int stage, const KeyPlace& w, uint32_t live) {
+            const uint32_t kd = stages_u + stage * kStage, vd = kd + kMmaKeys * kRowBytes;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int row = kChunks >= 32 ? i * 32 / kChunks : i * kPerLoad + lane / kChunks;
+                const int ch = lane % kChunks;
+                int64_t ko = w.k, vo = w.v;
+                if (whole_pages) {
+                    ko += row * s.k_token;
+                    vo += row * s.v_token;
+                } else {
+                    ko = __shfl_sync(0xffffffffu, w.k, row);
+                    vo = __shfl_sync(0xffffffffu, w.v, row);
+                }
+                const bool ok = (live >> row) & 1;
+                const uint32_t to = row * kRowBytes + (ch ^ (row & 7)) * 16;
+                const bool kok = ok && ch < ck, vok = ok && ch < cv;
+                cp_async16(kd + to, kok ? kh + ko + ch * 16 : a.kp, kok);
+                cp_async16(vd + to, vok ? vh + vo + ch * 16 : a.vp, vok);
+            }
+        };
+        uint32_t live[kMmaStages];
+        KeyPlace next;
+#pragma unroll
+        for (int p = 0; p < kMmaStages - 1; ++p) {
+            next = locate(k0 + p);
+            live[p] = live_keys(k0 + p, next);
+            if (k0 + p < k1) load(p, next, live[p]);
+            cp_async_commit();
+        }
+        next = locate(k0 + kMmaStages - 1);
+        int stage = 0;
+        for (int i = k0; i < k1; ++i) {
+            cp_async_wait<kMmaStages - 2>();
+            __syncwarp();
+            const uint32_t kd = stages_u + stage * kStage, vd = kd + kMmaKeys * kRowBytes;
+            const uint32_t mask = live[0];
+            {   // the stage read in the last step is free: load three tiles ahead
+                const int ahead = i + kMmaStages - 1, to = stage == 0 ? kMmaStages - 1 : stage - 1;
+                const uint32_t lv = live_keys(ahead, next);
+                if (ahead < k1) load(to, next, lv);
+                cp_async_commit();
+                next = locate(ahead + 1);
+#pragma unroll
+                for (int p = 0; p < kMmaStages - 2; ++p) live[p] = live[p + 1];
+                live[kMmaStages - 2] = lv;
+            }
+            // logits: keys 0..7 in x[0], 8..15 in x[1]
+            float x[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+            {
+                const int row = (lane & 7) + ((lane >> 4) << 3);
+                const uint32_t base = kd + row * kRowBytes;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    uint32_t f[4];
+                    ldmatrix4(f, base + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+                    if (SETS == 3) {
+                        mma16816(x[0], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[0], f[1]);
+                        mma16816(x[1], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[2], f[3]);
+                    } else {
+                        mma16816(x[0], q[k][0], q[k][0], q[k][1], q[k][1], f[0], f[1]);
+                        mma16816(x[1], q[k][0], q[k][0], q[k][1], q[k][1], f[2], f[3]);
+                    }
+                }
+            }
+            uint32_t w[kMine][2][3];                       // weights' terms: [row][key octet][term]
+#pragma unroll
+            for (int r = 0; r < kMine; ++r) {
+                float y[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        y[2 * n + e] = (mask >> (n * 8 + pair * 2 + e)) & 1 ? x[n][2 * r + e] * a.qscale
+                                                                            : -CUDART_INF_F;
+                if (a.logits) {
+                    const int g = quad + 8 * r;
+                    if (g < rows) {
+                        const int pos = i * kTile + warp * kMmaKeys;
+                        float* to = a.logits + ((int64_t)b * s.hq + g0 + g) * s.cap + pos;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = n * 8 + pair * 2 + e;
+                                if (pos + key < len) to[key] = y[2 * n + e];
+                            }
+                    }
+                }
+                float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // The reference follows the maximum only when it has grown by more than 2^8, which
+                // spares most steps the rescaling; weights up to 2^8 lose nothing in fp32.
+                const bool grow = top > m[r] + 8.f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? ex2(m[r] - top) : 1.f;
+                    if (grow) m[r] = top;
+                    l[r] *= f;
+                    if (SETS == 3) {
+#pragma unroll
+                        for (int n = 0; n < DP / 8; ++n) o[n][2 * r] *= f, o[n][2 * r + 1] *= f;
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[n][e] *= f;
+                    }
+                }
+                const float ref = m[r] == -CUDART_INF_F ? 0.f : m[r];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = ex2(y[e] - ref);
+                l[r] += (y[0] + y[1]) + (y[2] + y[3]);
+                split_bf16(y[0], y[1], w[r][0]);
+                split_bf16(y[2], y[3], w[r][1]);
+            }
+            // values
+            {
+                const int row = lane & 15;
+                const uint32_t base = vd + row * kRowBytes;
+                uint32_t p0 = 0, p1 = 0, p2 = 0, p3 = 0;
+                if (SETS == 1) {   // rows 0-3: term 0, 8-11: term 1, 4-7: term 2, 12-15: nothing
+                    const bool up = quad < 4;
+                    p0 = up ? w[0][0][0] : w[0][0][2]; p1 = up ? w[0][0][1] : 0u;
+                    p2 = up ? w[0][1][0] : w[0][1][2]; p3 = up ? w[0][1][1] : 0u;
+                }
+#pragma unroll
+                for (int n = 0; n < DP / 16; ++n) {
+                    uint32_t f[4];
+                    ldmatrix4t(f, base + (((2 * n + (lane >> 4)) ^ (row & 7)) << 4));
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        // The product of the 16 keys by itself, then an ordinary fp32 addition: the
+                        // tensor cores' own accumulation does not round to nearest, and over the
+                        // thousands of steps of a long cache its errors all point one way
+                        // (4.3e-6 of the output at 131072 keys, 0.9e-6 so).
+                        float z[4];
+                        const uint32_t b0 = f[2 * u], b1 = f[2 * u + 1];
+                        if (SETS == 1) {
+                            mma16816_new(z, p0, p1, p2, p3, b0, b1);
+                        } else if (SETS == 2) {
+                            mma16816_new(z, w[0][0][0], w[0][0][1], w[0][1][0], w[0][1][1], b0, b1);
+                            mma16816(z, w[0][0][2], 0u, w[0][1][2], 0u, b0, b1);
+                        } else {
+                            mma16816_new(z, w[0][0][0], w[kMine - 1][0][0], w[0][1][0], w[kMine - 1][1][0], b0, b1);
+                            mma16816(z, w[0][0][1], w[kMine - 1][0][1], w[0][1][1], w[kMine - 1][1][1], b0, b1);
+                            mma16816(z, w[0][0][2], w[kMine - 1][0][2], w[0][1][2], w[kMine - 1][1][2], b0, b1);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[2 * n + u][e] += z[e];
+                    }
+                }
+            }
+            stage = stage + 1 == kMmaStages ? 0 : stage + 1;
+            __syncwarp();
+        }
+        cp_async_wait<0>();
+        __syncthreads();
+        // the warps' sums into the stages, which are idle now: [warp][kRows][dv + 2]
+        float* merge = reinterpret_cast<float*>(smem);
+        const int ld = s.dv + 2;
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            const int g = quad + 8 * r;
+            float* row = merge + (warp * kRows + (g < kRows ? g : 0)) * ld;
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = o[n][2 * r + e];
+                    if (SETS != 3) v += o[n][2 + e];
+                    if (SETS == 1) v += __shfl_xor_sync(0xffffffffu, v, 16);
+                    const int col = n * 8 + pair * 2 + e;
+                    if (g < kRows && col < s.dv) row[col] = v;
+                }
+            }
+            if (g < kRows && pair == 0) {
+                row[s.dv] = m[r];
+                row[s.dv + 1] = l[r];
+            }
+        }
+        __syncthreads();
+        const bool whole = k0 == 0 && k1 == tiles && !a.csplits && !a.logits;
+        const int64_t unit = (int64_t)b * per_tile + in_b;
+        join_warps<kRows>(a, merge, whole ? nullptr : a.parts + (unit + c) * a.rows * c1_row(s.dv),
+                          (int64_t)b * s.hq + g0, rows);
         __syncthreads();
         t += k1 - k0;
         k0 = 0;
@@ -497,6 +859,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
     }
     const int len = checked_len(a.lens, b, s.cap, a.status);
     if (score && key0 >= len) return;
+    grid_dependency_wait();   // the partial rows (and everything before them) are there from here on
     const Place at = find_place<kJoinThreads>(s, a.lens, tile, per_tile, 0, a.blocks, b, a.status, place_sh);
     const int tiles = (len + tile - 1) / tile;
     float acc[kScoreKeys / kJoinThreads];
@@ -569,63 +932,112 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
+// Blocks of a kernel that the current device holds at once with `smem` bytes
+// each.  The answer (and the kernel's shared-memory limit, set before it is
+// asked for) is kept per kernel, device and size: the calls cost more than a
+// short attention's kernels do.
+wc_status resident_blocks(const void* kern, int smem, int* out) {
+    struct Entry { const void* kern; int dev, smem, blocks; };
+    constexpr int kEntries = 256;
+    static Entry table[kEntries];
+    static std::atomic<int> used{0};
+    static std::mutex lock;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WC_ERR_CUDA;
+    auto find = [&](int n) {
+        for (int i = 0; i < n; ++i)
+            if (table[i].kern == kern && table[i].dev == dev && table[i].smem == smem) return table[i].blocks;
+        return 0;
+    };
+    if ((*out = find(used.load(std::memory_order_acquire))) > 0) return WC_OK;
+    std::lock_guard<std::mutex> hold(lock);
+    const int n = used.load(std::memory_order_relaxed);
+    if ((*out = find(n)) > 0) return WC_OK;
+    int nsm = 0, per_sm = 0, limit = 0;
+    if (cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&limit, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+        return WC_ERR_CUDA;
+    // the device's whole limit, so that entries of other sizes stay valid
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit - (int)fa.sharedSizeBytes) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) != cudaSuccess || per_sm < 1)
+        return WC_ERR_CUDA;
+    *out = nsm * per_sm;
+    if (n < kEntries) {
+        table[n] = Entry{kern, dev, smem, *out};
+        used.store(n + 1, std::memory_order_release);
+    }
+    return WC_OK;
 }
 
-template <typename T, int RG, int NT, int NVI>
-wc_status run_simt(AttendArgs a, cudaStream_t st) {
-    auto kern = cache_attend_simt_kernel<T, RG, NT, NVI>;
-    const SimtSmem<NT, RG> L(a.s.d, a.s.dv, sizeof(T));
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total) != cudaSuccess)
-        return WC_ERR_CUDA;
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, L.total) != cudaSuccess)
-        return WC_ERR_CUDA;
-    const int nsm = sm_count();
-    if (nsm < 1 || per_sm < 1) return WC_ERR_CUDA;
-    constexpr int tile = kWarps * NT;
+// Launches one of the page kernels (its grid: as many blocks as the GPU holds
+// at once, or one per tile where there are fewer) and the join.
+wc_status run(AttendArgs a, void (*kern)(const AttendArgs), int smem, int tile, cudaStream_t st) {
+    int room = 0;
+    if (resident_blocks(reinterpret_cast<const void*>(kern), smem, &room) != WC_OK) return WC_ERR_CUDA;
     const int64_t most = (int64_t)a.s.B * a.s.hkv * a.row_tiles * ((a.s.cap + tile - 1) / tile);
-    a.blocks = (int)min(most, (int64_t)min(nsm * per_sm, kMaxBlocks));
+    a.blocks = (int)min(most, (int64_t)min(room, kMaxBlocks));
     const int64_t grid = a.blocks + (int64_t)a.csplits * a.s.B * a.s.hkv * a.row_tiles;
     if (grid > INT32_MAX) return WC_ERR_UNSUPPORTED;
-    kern<<<(unsigned)grid, kThreads, L.total, st>>>(a);
+    kern<<<(unsigned)grid, kThreads, smem, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
     const int64_t chunks = (a.s.cap + kScoreKeys - 1) / kScoreKeys;
     const int64_t join = (int64_t)a.s.B * a.s.hq + (a.scores ? chunks * a.s.B * a.s.hkv : 0);
     if (join > INT32_MAX) return WC_ERR_UNSUPPORTED;
-    cache_join_kernel<<<(unsigned)join, kJoinThreads, 0, st>>>(a, tile);
-    return cudaGetLastError() == cudaSuccess ? WC_OK : WC_ERR_CUDA;
+    // the join's blocks may start while the last page blocks run; they wait before they read partial rows
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)join);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel, a, tile) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
 }
 
-template <typename T, int RG, int NT>
-wc_status by_width(const AttendArgs& a, cudaStream_t st) {
-    return a.s.dv <= 128 ? run_simt<T, RG, NT, 1>(a, st) : run_simt<T, RG, NT, 2>(a, st);
+template <int RG, int NT>
+wc_status run_simt(const AttendArgs& a, cudaStream_t st) {
+    const int smem = SimtSmem<NT, RG>(a.s.d, a.s.dv, 4).total;
+    return a.s.dv <= 128 ? run(a, cache_attend_simt_kernel<RG, NT, 1>, smem, kWarps * NT, st)
+                         : run(a, cache_attend_simt_kernel<RG, NT, 2>, smem, kWarps * NT, st);
 }
 
-template <typename T, int RG>
+template <int RG>
 wc_status by_keys(const AttendArgs& a, cudaStream_t st) {
     // 16 keys a warp while two stages of them fit shared memory beside the rest (rows of up to 1024 bytes)
-    return (a.s.d + a.s.dv) * (int)sizeof(T) <= 1024 ? by_width<T, RG, 16>(a, st) : by_width<T, RG, 8>(a, st);
+    return (a.s.d + a.s.dv) * 4 <= 1024 ? run_simt<RG, 16>(a, st) : run_simt<RG, 8>(a, st);
 }
 
-template <typename T>
-wc_status by_rows(const AttendArgs& a, cudaStream_t st) {
-    switch (a.rows) {
-        case 1: return by_keys<T, 1>(a, st);
-        case 2: return by_keys<T, 2>(a, st);
-        case 4: return by_keys<T, 4>(a, st);
-        default: return by_keys<T, 8>(a, st);
-    }
+template <int DP, int SETS>
+wc_status run_mma(const AttendArgs& a, cudaStream_t st) {
+    constexpr int rows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
+    int smem = kWarps * kMmaStages * 2 * kMmaKeys * DP * 2;
+    if (a.csplits) smem = max(smem, SimtSmem<16, rows>(a.s.d, a.s.dv, 2).total);
+    return run(a, cache_attend_mma_kernel<DP, SETS>, smem, kWarps * kMmaKeys, st);
+}
+
+template <int DP>
+wc_status by_sets(const AttendArgs& a, cudaStream_t st) {
+    return a.rows == 4 ? run_mma<DP, 1>(a, st) : a.rows == 8 ? run_mma<DP, 2>(a, st) : run_mma<DP, 3>(a, st);
 }
 
 }  // namespace
 
 wc_status launch_attend(const AttendArgs& a, cudaStream_t st) {
-    return a.s.dtype == WC_BF16 ? by_rows<__nv_bfloat16>(a, st) : by_rows<float>(a, st);
+    if (a.s.dtype == WC_BF16) {
+        const int w = max(a.s.d, a.s.dv);
+        return w <= 64 ? by_sets<64>(a, st) : w <= 128 ? by_sets<128>(a, st) : by_sets<256>(a, st);
+    }
+    switch (a.rows) {
+        case 1: return by_keys<1>(a, st);
+        case 2: return by_keys<2>(a, st);
+        case 4: return by_keys<4>(a, st);
+        default: return by_keys<8>(a, st);
+    }
 }
 
 }  // namespace cache

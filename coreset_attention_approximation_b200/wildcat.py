@@ -405,9 +405,9 @@ class PagedCache:
         self.batch, self.max_pages = table.shape
         self.hkv, self.d, self.dv, self.hq = hkv, d, v_pages.shape[3], int(hq)
         self.cap = self.max_pages * page
+        self._on_device(v_pages, "v_pages")
         self.table = self._tensor(table, "table", (self.batch, self.max_pages), torch.int32)
         self.scores = None if scores is None else self._scores(scores, "scores")
-        self._on_device(v_pages, "v_pages")
         self.shape = WcCache(self.batch, self.hq, hkv, d, self.dv,
                              WC_BF16 if self.dtype == torch.bfloat16 else WC_F32, page, n_pages, self.max_pages,
                              scale, *_strides(k_pages), *_strides(v_pages))
@@ -417,6 +417,11 @@ class PagedCache:
         if self.device.type != "cuda":
             raise WildcatError(1, "PagedCache: the pages are on a GPU")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        # what every call passes on, looked up once (a decode step's calls are as short as their checks)
+        self._shape_ref = ctypes.byref(self.shape)
+        self._p_scores = None if scores is None else scores.data_ptr()
+        self._q_shape, self._o_shape = (self.batch, self.hq, self.d), (self.batch, self.hq, self.dv)
+        self._kept = (self.k_pages, self.v_pages, self.table, self.scores, self.ws)
 
     # ---- arguments
 
@@ -425,7 +430,7 @@ class PagedCache:
             raise WildcatError(1, f"PagedCache: {name} is on {t.device}, the pages on {self.device}")
 
     def _tensor(self, t, name, shape, dtype):
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
             raise WildcatError(1, f"PagedCache: {name} is a contiguous {dtype} tensor of shape {tuple(shape)}, got "
                                   f"{t.dtype} {tuple(t.shape)}")
         self._on_device(t, name)
@@ -436,27 +441,40 @@ class PagedCache:
 
     def _rows(self, t, name, shape):
         """A strided tensor of rows in the pages' type."""
-        if tuple(t.shape) != tuple(shape) or t.dtype != self.dtype:
+        if t.shape != shape or t.dtype != self.dtype:
             raise WildcatError(1, f"PagedCache: {name} is a {self.dtype} tensor of shape {tuple(shape)}, got "
                                   f"{t.dtype} {tuple(t.shape)}")
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        if t.stride(-1) != 1:
             raise WildcatError(1, f"PagedCache: rows of {name} are contiguous")
         self._on_device(t, name)
         return t
 
-    def _launch(self, stream, call, what, tensors):
-        """`call(stream handle)` on the given stream, or the device's current
-        one.  The caching allocator is told of the tensors' use on a given one."""
-        current = torch.cuda.current_stream(self.device)
-        s = current if stream is None else stream
-        if s.device != self.device:
-            raise WildcatError(1, f"{what}: the stream is another device's")
-        if s != current:
-            for t in tensors:
+    def _launch(self, call, what, stream, args, tensors):
+        """call(*args, stream) on the given stream, or the device's current
+        one, with the pages' device current.  The caching allocator is told of
+        the tensors' use on a given stream."""
+        s = torch.cuda.current_stream(self.device)
+        if stream is not None and stream != s:
+            if stream.device != self.device:
+                raise WildcatError(1, f"{what}: the stream is another device's")
+            for t in tensors + self._kept:
                 if t is not None:
-                    t.record_stream(s)
-        with torch.cuda.device(self.device):
-            _check(call(ctypes.c_void_p(s.cuda_stream)), what)
+                    t.record_stream(stream)
+            s = stream
+        if torch.cuda.current_device() == self.device.index:
+            code = call(*args, s.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                code = call(*args, s.cuda_stream)
+        if code != 0:
+            raise WildcatError(code, what)
+
+    def _empty(self, shape, dtype, stream):
+        """An output, allocated for the stream that writes it."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
 
     # ---- calls
 
@@ -467,17 +485,17 @@ class PagedCache:
         steps of 16 bytes.  Rows beyond the cache's end are not written and
         reported by `check()`."""
         t = K.shape[2] if K.dim() == 4 else -1
-        K = self._rows(K, "K", (self.batch, self.hkv, t, self.d))
-        V = self._rows(V, "V", (self.batch, self.hkv, t, self.dv))
-        pos = self._tensor(pos, "pos", (self.batch,), torch.int32)
+        self._rows(K, "K", (self.batch, self.hkv, t, self.d))
+        self._rows(V, "V", (self.batch, self.hkv, t, self.dv))
+        self._tensor(pos, "pos", (self.batch,), torch.int32)
         if count is not None:
-            count = self._tensor(count, "count", (self.batch,), torch.int32)
-        ws, ks, vs = self.ws, WcRowStrides(*_strides(K)), WcRowStrides(*_strides(V))
-        self._launch(stream, lambda s: lib().wc_cache_append(
-            ctypes.byref(self.shape), t, _ptr(K), ctypes.byref(ks), _ptr(V), ctypes.byref(vs), _ptr(pos),
-            _ptr(count), _ptr(self.k_pages), _ptr(self.v_pages), _ptr(self.table), _ptr(self.scores), _ptr(ws),
-            ws.numel(), s), "wc_cache_append", (K, V, pos, count, self.k_pages, self.v_pages, self.table,
-                                                self.scores, ws))
+            self._tensor(count, "count", (self.batch,), torch.int32)
+        ks, vs = WcRowStrides(*_strides(K)), WcRowStrides(*_strides(V))
+        self._launch(lib().wc_cache_append, "wc_cache_append", stream,
+                     (self._shape_ref, t, K.data_ptr(), ctypes.byref(ks), V.data_ptr(), ctypes.byref(vs),
+                      pos.data_ptr(), None if count is None else count.data_ptr(), self.k_pages.data_ptr(),
+                      self.v_pages.data_ptr(), self.table.data_ptr(), self._p_scores, self.ws.data_ptr(),
+                      self.ws.numel()), (K, V, pos, count))
 
     def attend(self, Q, lens, *, coreset=None, accumulate=False, return_lse=False, out=None, stream=None):
         """Attention of one new token per sequence: Q [B, Hq, d] over the first
@@ -485,8 +503,8 @@ class PagedCache:
         them (as `weights` and `select` return them; rank None: all r rows).
         Returns out [B, Hq, dv] fp32, or (out, lse [B, Hq]).  accumulate: adds
         each key's attention weight, summed over its queries, to `scores`."""
-        Q = self._rows(Q, "Q", (self.batch, self.hq, self.d))
-        lens = self._tensor(lens, "lens", (self.batch,), torch.int32)
+        self._rows(Q, "Q", self._q_shape)
+        self._tensor(lens, "lens", (self.batch,), torch.int32)
         if accumulate and self.scores is None:
             raise WildcatError(1, "PagedCache.attend: accumulate needs scores")
         Ks = W = rank = None
@@ -494,23 +512,22 @@ class PagedCache:
         if coreset is not None:
             Ks, W, rank = coreset
             r = Ks.shape[2] if Ks.dim() == 4 else -1
-            Ks = self._tensor(Ks, "Ks", (self.batch, self.hkv, r, self.d), self.dtype)
-            W = self._tensor(W, "W", (self.batch, self.hkv, r, self.dv + 1), torch.float32)
+            self._tensor(Ks, "Ks", (self.batch, self.hkv, r, self.d), self.dtype)
+            self._tensor(W, "W", (self.batch, self.hkv, r, self.dv + 1), torch.float32)
             if rank is not None:
-                rank = self._tensor(rank, "rank", (self.batch, self.hkv), torch.int32)
-        ws = self.ws
-        with torch.cuda.device(self.device), torch.cuda.stream(stream):
-            if out is None:
-                out = torch.empty(self.batch, self.hq, self.dv, dtype=torch.float32, device=self.device)
-            else:
-                out = self._tensor(out, "out", (self.batch, self.hq, self.dv), torch.float32)
-            lse = torch.empty(self.batch, self.hq, dtype=torch.float32, device=self.device) if return_lse else None
-        scores = self.scores if accumulate else None
-        self._launch(stream, lambda s: lib().wc_cache_attend(
-            ctypes.byref(self.shape), _ptr(Q), Q.stride(0), Q.stride(1), _ptr(self.k_pages), _ptr(self.v_pages),
-            _ptr(self.table), _ptr(lens), r, _ptr(Ks), _ptr(W), _ptr(rank), _ptr(out), _ptr(lse), _ptr(scores),
-            _ptr(ws), ws.numel(), s), "wc_cache_attend",
-            (Q, lens, Ks, W, rank, out, scores, self.k_pages, self.v_pages, self.table, ws))
+                self._tensor(rank, "rank", (self.batch, self.hkv), torch.int32)
+        if out is None:
+            out = self._empty(self._o_shape, torch.float32, stream)
+        else:
+            self._tensor(out, "out", self._o_shape, torch.float32)
+        lse = self._empty((self.batch, self.hq), torch.float32, stream) if return_lse else None
+        sq = Q.stride()
+        self._launch(lib().wc_cache_attend, "wc_cache_attend", stream,
+                     (self._shape_ref, Q.data_ptr(), sq[0], sq[1], self.k_pages.data_ptr(), self.v_pages.data_ptr(),
+                      self.table.data_ptr(), lens.data_ptr(), r, None if r == 0 else Ks.data_ptr(),
+                      None if r == 0 else W.data_ptr(), None if rank is None else rank.data_ptr(), out.data_ptr(),
+                      None if lse is None else lse.data_ptr(), self._p_scores if accumulate else None,
+                      self.ws.data_ptr(), self.ws.numel()), (Q, lens, Ks, W, rank, out, lse))
         return (out, lse) if return_lse else out
 
     def evict(self, lens, keep, *, sink=0, recent=0, into=None, scores_into=None, lens_out=None, stream=None):
@@ -524,28 +541,27 @@ class PagedCache:
         (lens_out may be lens itself).  A sequence that cannot be moved (a page
         outside the pool, a page to be written that is named twice) stays as it
         is; `check()` reports it."""
-        lens = self._tensor(lens, "lens", (self.batch,), torch.int32)
+        self._tensor(lens, "lens", (self.batch,), torch.int32)
         if self.scores is None:
             raise WildcatError(1, "PagedCache.evict: needs scores")
         if into is not None:
-            into = self._tensor(into, "into", (self.batch, self.max_pages), torch.int32)
+            self._tensor(into, "into", (self.batch, self.max_pages), torch.int32)
         if scores_into is not None:
-            scores_into = self._scores(scores_into, "scores_into")
+            self._scores(scores_into, "scores_into")
         keep, sink, recent = int(keep), int(sink), int(recent)
         if not (1 <= keep <= self.cap and sink >= 0 and recent >= 0 and sink + recent <= keep):
             raise WildcatError(1, "PagedCache.evict: 1 <= keep <= capacity, sink + recent <= keep")
-        ws = self.ws
-        with torch.cuda.device(self.device), torch.cuda.stream(stream):
-            idx = torch.empty(self.batch, self.hkv, keep, dtype=torch.int32, device=self.device)
-            if lens_out is None:
-                lens_out = torch.empty(self.batch, dtype=torch.int32, device=self.device)
-            else:
-                lens_out = self._tensor(lens_out, "lens_out", (self.batch,), torch.int32)
-        self._launch(stream, lambda s: lib().wc_cache_evict(
-            ctypes.byref(self.shape), keep, sink, recent, _ptr(self.k_pages), _ptr(self.v_pages), _ptr(self.table),
-            _ptr(into), _ptr(lens), _ptr(self.scores), _ptr(scores_into), _ptr(idx), _ptr(lens_out), _ptr(ws),
-            ws.numel(), s), "wc_cache_evict",
-            (lens, into, scores_into, lens_out, self.scores, self.k_pages, self.v_pages, self.table, ws))
+        idx = self._empty((self.batch, self.hkv, keep), torch.int32, stream)
+        if lens_out is None:
+            lens_out = self._empty((self.batch,), torch.int32, stream)
+        else:
+            self._tensor(lens_out, "lens_out", (self.batch,), torch.int32)
+        self._launch(lib().wc_cache_evict, "wc_cache_evict", stream,
+                     (self._shape_ref, keep, sink, recent, self.k_pages.data_ptr(), self.v_pages.data_ptr(),
+                      self.table.data_ptr(), None if into is None else into.data_ptr(), lens.data_ptr(),
+                      self._p_scores, None if scores_into is None else scores_into.data_ptr(), idx.data_ptr(),
+                      lens_out.data_ptr(), self.ws.data_ptr(), self.ws.numel()),
+                     (lens, into, scores_into, idx, lens_out))
         return dict(idx=idx, lens=lens_out)
 
     def check(self, stream=None) -> int:
