@@ -1,7 +1,10 @@
 // cache.cu — the paged cache's C ABI (include/wildcat.h): argument checks,
 // workspace layout, append and evict.  The attention is in cache_attend.cu.
+#include <cooperative_groups.h>
 #include <math.h>
 #include <nvtx3/nvToolsExt.h>
+
+#include <atomic>
 
 #include "wc_cache.cuh"
 
@@ -53,14 +56,14 @@ wc_status make_view(const wc_cache* in, View* o) {
 }
 
 // Query rows of one unit of the attention's work.
-static int rows_of(const View& s) {
+int rows_of(const View& s) {
     if (s.dtype == WC_BF16) return s.group > 8 ? 16 : s.group > 4 ? 8 : 4;
     return s.group >= 5 ? 8 : s.group >= 3 ? 4 : s.group;
 }
 
 // Coreset rows of one block: whole 64-row steps, about kCoresetBlocks blocks over all units (at
 // most units + kCoresetBlocks, which the workspace holds).
-static int coreset_split_len(const View& s, int r, int row_tiles) {
+int coreset_split_len(const View& s, int r, int row_tiles) {
     const int64_t units = (int64_t)s.B * s.hkv * row_tiles, steps = (r + 63) / 64;
     const int64_t want = (kCoresetBlocks + units - 1) / units, splits = want < steps ? want : steps;
     return (int)((steps + splits - 1) / splits) * 64;
@@ -101,40 +104,91 @@ struct AppendArgs {
     int* status;
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyRows = 16;    // rows of one warp's step
 
-// One warp a row (sequence, new row, kv head): its key and its value in 16-byte
-// pieces.  A plain copy, bound by the bytes it moves.
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
-    const View& s = a.s;
-    const int64_t rows = (int64_t)s.B * a.t * s.hkv;
+// Where 16 rows come from and go to: lane j < 16 holds row j's addresses.
+struct RowCopy {
+    const char *ks, *vs;
+    char *kd, *vd;
+    bool ok;
+};
+
+__device__ __forceinline__ const char* shfl_ptr(const char* p, int from) {
+    return reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), from));
+}
+
+// One warp copies 16 key rows and 16 value rows in 16-byte pieces, four pieces a
+// lane in flight; rows that are not `ok` are skipped.  A copy, bound by the
+// bytes it moves; the addresses of 16 rows are worked out once, a row a lane
+// (one row a warp, each with its own lookups, reached half of the rate).
+__device__ __forceinline__ void copy_rows(const RowCopy& r, int ck, int cv) {
     const int lane = threadIdx.x & 31;
-    const int ck = s.d * s.esize / 16, cv = s.dv * s.esize / 16;
-    for (int64_t i = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5); i < rows;
-         i += (int64_t)gridDim.x * (kAppendThreads / 32)) {
-        const int h = (int)(i % s.hkv);
-        const int64_t bj = i / s.hkv;
-        const int j = (int)(bj % a.t), b = (int)(bj / a.t);
-        const int n = a.count ? __ldg(a.count + b) : a.t;
-        if (n < 0 || n > a.t) record_status(a.status, WC_ERR_BOUNDS);
-        if (j >= n) continue;
-        const int64_t at = (int64_t)__ldg(a.pos + b) + j;
-        if (at < 0 || at >= s.cap) {
+    const uint32_t live = __ballot_sync(0xffffffffu, r.ok) & 0xffffu;
+    if (!live) return;
+    const int n = 32 - __clz(live);                  // rows up to the last live one
+    // x / c for x < 16 * 64 and c <= 64 as (x * ceil(2^16 / c)) >> 16: off by less than 1024 / 2^16 < 1 / c
+    const uint32_t mk = (65535u + ck) / ck, mv = (65535u + cv) / cv;
+    const int nk = n * ck, total = nk + n * cv;
+    for (int base = 0; base < total; base += 128) {
+        uint4 x[4];
+        char* to[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = base + u * 32 + lane;
+            const bool key = i < nk;
+            const uint32_t j = key ? i : i - nk;
+            const int row = min((int)((j * (key ? mk : mv)) >> 16), kCopyRows - 1);
+            const int at = (int)j - row * (key ? ck : cv);
+            // one shuffle a pointer: a lane's source and target are both of its row
+            const char* ks = shfl_ptr(r.ks, row);
+            const char* vs = shfl_ptr(r.vs, row);
+            const char* kd = shfl_ptr(r.kd, row);
+            const char* vd = shfl_ptr(r.vd, row);
+            const bool go = i < total && ((live >> row) & 1);
+            to[u] = go ? const_cast<char*>(key ? kd : vd) + at * 16 : nullptr;
+            if (go) x[u] = *reinterpret_cast<const uint4*>((key ? ks : vs) + at * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (to[u]) *reinterpret_cast<uint4*>(to[u]) = x[u];
+    }
+}
+
+// One warp per 16 new rows of one (sequence, kv head).
+__global__ void __launch_bounds__(kCopyThreads) cache_append_kernel(const AppendArgs a) {
+    const View& s = a.s;
+    const int lane = threadIdx.x & 31, groups = (a.t + kCopyRows - 1) / kCopyRows;
+    const int64_t items = (int64_t)s.B * s.hkv * groups;
+    for (int64_t i = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); i < items;
+         i += (int64_t)gridDim.x * (kCopyThreads / 32)) {
+        const int64_t unit = i / groups;
+        const int j = (int)(i - unit * groups) * kCopyRows + lane, b = (int)(unit / s.hkv), h = (int)(unit - (int64_t)b * s.hkv);
+        int n = a.count ? __ldg(a.count + b) : a.t;
+        if (n < 0 || n > a.t) {
             record_status(a.status, WC_ERR_BOUNDS);
-            continue;
+            n = min(max(n, 0), a.t);
         }
-        const int tp = (int)at / s.page, slot = (int)at - tp * s.page;
-        const int pg = checked_page(s, s.table, b, tp, a.status);
-        if (pg < 0) continue;
-        const uint4* ks = reinterpret_cast<const uint4*>(a.K + b * a.k_batch + h * a.k_head + j * a.k_row);
-        const uint4* vs = reinterpret_cast<const uint4*>(a.V + b * a.v_batch + h * a.v_head + j * a.v_row);
-        uint4* kd = reinterpret_cast<uint4*>(a.kp + pg * s.k_page + h * s.k_head + slot * s.k_token);
-        uint4* vd = reinterpret_cast<uint4*>(a.vp + pg * s.v_page + h * s.v_head + slot * s.v_token);
-        for (int c = lane; c < ck + cv; c += 32) {
-            if (c < ck) kd[c] = ks[c];
-            else vd[c - ck] = vs[c - ck];
+        RowCopy r{nullptr, nullptr, nullptr, nullptr, false};
+        if (lane < kCopyRows && j < n) {
+            const int64_t at = (int64_t)__ldg(a.pos + b) + j;
+            if (at < 0 || at >= s.cap) {
+                record_status(a.status, WC_ERR_BOUNDS);
+            } else {
+                const int tp = (int)at / s.page, slot = (int)at - tp * s.page;
+                const int pg = checked_page(s, s.table, b, tp, a.status);
+                if (pg >= 0) {
+                    r.ks = a.K + b * a.k_batch + h * a.k_head + j * a.k_row;
+                    r.vs = a.V + b * a.v_batch + h * a.v_head + j * a.v_row;
+                    r.kd = a.kp + pg * s.k_page + h * s.k_head + slot * s.k_token;
+                    r.vd = a.vp + pg * s.v_page + h * s.v_head + slot * s.v_token;
+                    r.ok = true;
+                    if (a.scores) a.scores[((int64_t)b * s.hkv + h) * s.cap + at] = 0.f;
+                }
+            }
         }
-        if (a.scores && lane == 0) a.scores[((int64_t)b * s.hkv + h) * s.cap + at] = 0.f;
+        __syncwarp();
+        copy_rows(r, s.d * s.esize / 16, s.dv * s.esize / 16);
     }
 }
 
@@ -152,24 +206,6 @@ struct EvictArgs {
     int* status;
 };
 
-// References to every page: one for each page a sequence's tokens use, one for
-// each page of `into` that it will write.
-__global__ void cache_mark_kernel(const EvictArgs a) {
-    const View& s = a.s;
-    const int b = blockIdx.y;
-    const int len = checked_len(a.lens, b, s.cap, a.status), kept = min(len, a.keep);
-    const int used = (len + s.page - 1) / s.page, written = a.into ? (kept + s.page - 1) / s.page : 0;
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < used + written; i += gridDim.x * blockDim.x) {
-        const int32_t* row = (i < used ? s.table : a.into) + (int64_t)b * s.max_pages;
-        const int p = row[i < used ? i : i - used];
-        if ((unsigned)p < (unsigned)s.n_pages) atomicAdd(a.marks + p, 1);
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        a.ws_lens[2 * b] = len;
-        a.ws_lens[2 * b + 1] = kept;
-    }
-}
-
 // Order-preserving bits of a score: larger score, larger key; NaN as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t score_key(float x) {
     if (isnan(x)) x = -CUDART_INF_F;
@@ -178,105 +214,182 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 
 constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectCluster = 8;             // blocks that may share one (sequence, kv head)
+constexpr int kSelectSlice = 4096;            // positions of a block before another one joins it
+constexpr int kSelectHeld = 40960;            // keys a block holds in shared memory, at most
 
-// Inclusive sum over the block's threads; sh holds one int per warp and stays
-// the block's own until the next call's first barrier.
-__device__ __forceinline__ int block_scan(int v, int* sh, int* total) {
+// References to the pages of sequence b: one for each page its tokens use, one
+// for each page of `into` that it will write.
+__device__ __forceinline__ void mark_pages(const EvictArgs& a, int b, int len, int kept, int first, int step) {
+    const View& s = a.s;
+    const int used = (len + s.page - 1) / s.page, written = a.into ? (kept + s.page - 1) / s.page : 0;
+    for (int i = first; i < used + written; i += step) {
+        const int32_t* row = (i < used ? s.table : a.into) + (int64_t)b * s.max_pages;
+        const int p = row[i < used ? i : i - used];
+        if ((unsigned)p < (unsigned)s.n_pages) atomicAdd(a.marks + p, 1);
+    }
+}
+
+// Inclusive sum over the block's threads; sh holds one int per warp.
+__device__ __forceinline__ int block_scan(int v, int* sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
-    __syncthreads();
     if (lane == 31) sh[warp] = v;
     __syncthreads();
-    int w = lane < kSelectThreads / 32 ? sh[lane] : 0;
+    int w = sh[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += u;
     }
-    *total = __shfl_sync(0xffffffffu, w, 31);
     const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
     return v + (warp > 0 ? before : 0);
 }
 
-// The kept positions of one (sequence, kv head): a radix select of the
-// threshold score in three passes over the keys (11, 11 and 10 bits, a
-// histogram each), then the positions in order.
-__global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const EvictArgs a) {
-    __shared__ int hist[2048];
-    __shared__ int sh[32];
+// The kept positions of one (sequence, kv head), by a cluster of 1 to 8 blocks,
+// each with a stretch of the positions.  The threshold score (the want-th
+// largest of those that compete) comes from a radix select in three passes (11,
+// 11 and 10 bits of the ordered keys): each block counts its own keys, every
+// block adds the cluster's histograms through distributed shared memory and
+// finds the same bin.  Then each warp counts what it keeps of its own stretch,
+// and writes the positions in order behind those of the warps before it.  The
+// keys are read from memory once and held in shared memory where they fit.
+// Bound by the latency of the passes (a few barriers each) for the lengths of
+// real caches.
+__global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const EvictArgs a, int held) {
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ int hist[3][2048];
+    __shared__ int sh[kSelectWarps];
+    __shared__ int counts[kSelectWarps][2];
+    __shared__ int block_counts[2];
     __shared__ uint32_t s_bin;
     __shared__ int s_left;
+    grid_dependents_launch();
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const View& s = a.s;
-    const int h = blockIdx.x % s.hkv, b = blockIdx.x / s.hkv, tid = threadIdx.x;
-    const int len = a.ws_lens[2 * b], kept = a.ws_lens[2 * b + 1];
-    int32_t* idx = a.idx + ((int64_t)b * s.hkv + h) * a.keep;
-    for (int i = kept + tid; i < a.keep; i += kSelectThreads) idx[i] = -1;
-    if (len <= a.keep) {
-        for (int i = tid; i < kept; i += kSelectThreads) idx[i] = i;
-        return;
+    const int unit = blockIdx.x / ranks, h = unit % s.hkv, b = unit / s.hkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int len = checked_len(a.lens, b, s.cap, a.status), kept = min(len, a.keep);
+    if (h == 0) {
+        mark_pages(a, b, len, kept, rank * kSelectThreads + tid, ranks * kSelectThreads);
+        if (rank == 0 && tid == 0) {
+            a.ws_lens[2 * b] = len;
+            a.ws_lens[2 * b + 1] = kept;
+        }
     }
-    const float* x = a.scores + ((int64_t)b * s.hkv + h) * s.cap;
-    const int first = a.sink, last = len - a.recent;
-    const int want = a.keep - a.sink - a.recent;   // of the positions [first, last); fewer than there are
+    int32_t* idx = a.idx + (int64_t)unit * a.keep;
+    for (int i = kept + rank * kSelectThreads + tid; i < a.keep; i += ranks * kSelectThreads) idx[i] = -1;
+    if (len <= a.keep) {
+        for (int i = rank * kSelectThreads + tid; i < kept; i += ranks * kSelectThreads) idx[i] = i;
+        return;   // every block of the cluster does
+    }
+    const float* x = a.scores + (int64_t)unit * s.cap;
+    const int per = ((len + ranks - 1) / ranks + 31) / 32 * 32;
+    const int lo = min(rank * per, len), hi = min(lo + per, len);
+    const int first = a.sink, last = len - a.recent;   // the positions that compete
+    const int want = a.keep - a.sink - a.recent;       // of them kept: fewer than there are
+    const bool hold = per <= held;
+    for (int i = tid; i < 3 * 2048; i += kSelectThreads) (&hist[0][0])[i] = 0;
+    auto key = [&](int i) { return hold ? keys[i - lo] : score_key(x[i]); };
+    if (hold)
+        for (int i = lo + tid; i < hi; i += kSelectThreads) keys[i - lo] = score_key(x[i]);
     uint32_t prefix = 0, mask = 0;
     int left = want;
+    __syncthreads();
     if (want > 0) {
         const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
+#pragma unroll
         for (int pass = 0; pass < 3; ++pass) {
             const int bins = 1 << bits[pass];
-            for (int i = tid; i < 2048; i += kSelectThreads) hist[i] = 0;
-            __syncthreads();
-            for (int i = first + tid; i < last; i += kSelectThreads) {
-                const uint32_t k = score_key(x[i]);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shifts[pass]) & (bins - 1)], 1);
+            for (int i = max(lo, first) + tid; i < min(hi, last); i += kSelectThreads) {
+                const uint32_t k = key(i);
+                if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shifts[pass]) & (bins - 1)], 1);
             }
-            __syncthreads();
+            cluster.sync();
             // from the top bin down: the bin in which the `left`-th key lies
-            const int hi = bins - 1 - 2 * tid, n1 = hi >= 0 ? hist[hi] : 0, n0 = hi >= 1 ? hist[hi - 1] : 0;
-            int total;
-            const int incl = block_scan(n1 + n0, sh, &total), before = incl - n1 - n0;
+            const int up = bins - 1 - 2 * tid;
+            int n1 = 0, n0 = 0;
+            if (up >= 1)
+                for (int r = 0; r < ranks; ++r) {
+                    const int2 v = *reinterpret_cast<const int2*>(cluster.map_shared_rank(&hist[pass][up - 1], r));
+                    n0 += v.x;
+                    n1 += v.y;
+                }
+            const int incl = block_scan(n1 + n0, sh), before = incl - n1 - n0;
             if (before < left && left <= incl) {
-                const bool up = left <= before + n1;
-                s_bin = up ? hi : hi - 1;
-                s_left = left - before - (up ? 0 : n1);
+                const bool top = left <= before + n1;
+                s_bin = top ? up : up - 1;
+                s_left = left - before - (top ? 0 : n1);
             }
             __syncthreads();
             prefix |= s_bin << shifts[pass];
             mask |= (uint32_t)(bins - 1) << shifts[pass];
             left = s_left;
-            __syncthreads();
         }
     }
-    // keys above `prefix` are kept, and the first `left` equal to it
-    int base = 0, ties = 0;
-    for (int at = 0; at < len; at += kSelectThreads) {
-        const int i = at + tid;
-        int above = 0, tie = 0;
-        if (i < len) {
-            if (i < first || i >= last) above = 1;
-            else if (want > 0) {
-                const uint32_t k = score_key(x[i]);
-                above = k > prefix;
-                tie = k == prefix;
-            }
+    // kept: the positions that do not compete, the keys above `prefix`, and the first `left` equal to it
+    const int span = ((hi - lo + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int w0 = min(lo + warp * span, hi), w1 = min(w0 + span, hi);
+    auto judge = [&](int i, bool& above, bool& tie) {
+        above = tie = false;
+        if (i >= w1) return;
+        if (i < first || i >= last) above = true;
+        else if (want > 0) {
+            const uint32_t k = key(i);
+            above = k > prefix;
+            tie = k == prefix;
         }
-        int total;
-        const int incl = block_scan(above | tie << 16, sh, &total);
-        const int tie_rank = ties + (incl >> 16) - tie;              // ties before this one
-        const int tie_before = min(tie_rank, left) - min(ties, left);  // of them kept, in this stretch
-        if (above || (tie && tie_rank < left)) idx[base + (incl & 0xffff) - above + tie_before] = i;
-        const int all_ties = total >> 16;
-        base += (total & 0xffff) + min(ties + all_ties, left) - min(ties, left);
-        ties += all_ties;
+    };
+    int n_above = 0, n_tie = 0;
+    for (int i = w0; i < w1; i += 32) {
+        bool above, tie;
+        judge(i + lane, above, tie);
+        n_above += __popc(__ballot_sync(0xffffffffu, above));
+        n_tie += __popc(__ballot_sync(0xffffffffu, tie));
     }
+    if (lane == 0) counts[warp][0] = n_above, counts[warp][1] = n_tie;
+    __syncthreads();
+    if (warp == 0) {
+        int u = counts[lane][0], v = counts[lane][1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            u += __shfl_xor_sync(0xffffffffu, u, o);
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+        }
+        if (lane == 0) block_counts[0] = u, block_counts[1] = v;
+    }
+    cluster.sync();
+    int above_before = 0, ties_before = 0;
+    for (int r = 0; r < rank; ++r) {
+        const int* c = cluster.map_shared_rank(block_counts, r);
+        above_before += c[0];
+        ties_before += c[1];
+    }
+    for (int w = 0; w < warp; ++w) above_before += counts[w][0], ties_before += counts[w][1];
+    int at = above_before + min(ties_before, left);
+    for (int i = w0; i < w1; i += 32) {
+        bool above, tie;
+        judge(i + lane, above, tie);
+        const uint32_t below = (1u << lane) - 1, ties = __ballot_sync(0xffffffffu, tie);
+        const bool keep = above || (tie && ties_before + __popc(ties & below) < left);
+        const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
+        if (keep) idx[at + __popc(keeps & below)] = i + lane;
+        at += __popc(keeps);
+        ties_before += __popc(ties);
+    }
+    cluster.sync();   // no block leaves while another may read its shared memory
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 64 * 1024;   // rows staged at a time
+constexpr int kMoveBytes = 64 * 1024;   // in place: bytes staged at a time
+constexpr int kMoveSlice = 64;          // in place: bytes of a row that one block moves
 
 // Whether a sequence's move is refused, and the reason recorded: a page
 // outside the pool, or a page to be written that is named more than once.
@@ -301,71 +414,154 @@ __device__ bool refused(const EvictArgs& a, int b, int len, int kept) {
     return any1 || any2;
 }
 
-// Moves the kept rows of one (sequence, kv head).  blockIdx.z: 0 keys, 1
-// values, 2 scores.  In place the target of kept row j is position j and its
-// source idx[j] >= j, so a block that works upwards, reading a stretch of rows
-// whole before it writes it, never writes a row that is still to be read.
-__global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArgs a) {
-    extern __shared__ __align__(16) char stage[];
+// The scores of one (sequence, kv head), a stretch read whole before it is
+// written (see move_in_place), its lengths, and -1 in idx where refused.
+__device__ void move_scores(const EvictArgs& a, int b, int h, int len, int kept, bool no, char* stage) {
     const View& s = a.s;
-    const int h = blockIdx.x, b = blockIdx.y, what = blockIdx.z, tid = threadIdx.x;
-    const int len = a.ws_lens[2 * b], kept = a.ws_lens[2 * b + 1];
-    const bool no = refused(a, b, len, kept);
-    int32_t* idx = a.idx + ((int64_t)b * s.hkv + h) * a.keep;
-    if (what == 2) {
-        if (h == 0 && tid == 0) a.lens_out[b] = no ? len : kept;
-        if (no)   // (the blocks that move keys and values are refused too and do not read idx)
-            for (int j = tid; j < a.keep; j += kMoveThreads) idx[j] = -1;
-        if (!no && (len > kept || a.scores_into != a.scores)) {
-            const float* from = a.scores + ((int64_t)b * s.hkv + h) * s.cap;
-            float* to = a.scores_into + ((int64_t)b * s.hkv + h) * s.cap;
-            float* sh = reinterpret_cast<float*>(stage);
-            constexpr int kChunk = kMoveBytes / 4;
-            for (int j0 = 0; j0 < kept; j0 += kChunk) {
-                const int n = min(kChunk, kept - j0);
-                for (int j = tid; j < n; j += kMoveThreads) sh[j] = from[idx[j0 + j]];
-                __syncthreads();
-                for (int j = tid; j < n; j += kMoveThreads) to[j0 + j] = sh[j];
-                __syncthreads();
-            }
-        }
+    const int64_t unit = (int64_t)b * s.hkv + h;
+    int32_t* idx = a.idx + unit * a.keep;
+    if (h == 0 && threadIdx.x == 0) a.lens_out[b] = no ? len : kept;
+    if (no) {   // (the blocks that move rows are refused too and do not read idx)
+        for (int j = threadIdx.x; j < a.keep; j += kMoveThreads) idx[j] = -1;
         return;
     }
-    if (no || (len <= kept && !a.into)) return;
-    const int row_bytes = (what ? s.dv : s.d) * s.esize, ch = row_bytes / 16;
-    char* pool = (what ? a.vp : a.kp) + h * (what ? s.v_head : s.k_head);
-    const int64_t page_st = what ? s.v_page : s.k_page, token_st = what ? s.v_token : s.k_token;
-    const int32_t* from = s.table + (int64_t)b * s.max_pages;
-    const int32_t* to = (a.into ? a.into : s.table) + (int64_t)b * s.max_pages;
-    const int rows = kMoveBytes / row_bytes;
-    uint4* sh = reinterpret_cast<uint4*>(stage);
-    for (int j0 = 0; j0 < kept; j0 += rows) {
-        const int n = min(rows, kept - j0) * ch;
-        for (int i = tid; i < n; i += kMoveThreads) {
-            const int j = i / ch, c = i - j * ch, at = idx[j0 + j], tp = at / s.page;
-            sh[i] = reinterpret_cast<const uint4*>(pool + from[tp] * page_st + (at - tp * s.page) * token_st)[c];
-        }
+    if (len <= kept && a.scores_into == a.scores) return;
+    const float* from = a.scores + unit * s.cap;
+    float* to = a.scores_into + unit * s.cap;
+    float* sh = reinterpret_cast<float*>(stage);
+    constexpr int kChunk = kMoveBytes / 4;
+    for (int j0 = 0; j0 < kept; j0 += kChunk) {
+        const int n = min(kChunk, kept - j0);
+#pragma unroll 4
+        for (int j = threadIdx.x; j < n; j += kMoveThreads) sh[j] = from[idx[j0 + j]];
         __syncthreads();
-        for (int i = tid; i < n; i += kMoveThreads) {
-            const int j = i / ch, c = i - j * ch, at = j0 + j, tp = at / s.page;
-            reinterpret_cast<uint4*>(pool + to[tp] * page_st + (at - tp * s.page) * token_st)[c] = sh[i];
-        }
+        for (int j = threadIdx.x; j < n; j += kMoveThreads) to[j0 + j] = sh[j];
         __syncthreads();
     }
 }
 
+// In place: 64 bytes of every kept row of one (sequence, kv head) per block.
+// The target of kept row j is position j and its source idx[j] >= j, so a
+// block that works upwards, reading a stretch of rows whole before it writes
+// it, never writes a row that is still to be read.  The slices let eight
+// blocks and more share a head whose rows have to move in order.
+__device__ void move_in_place(const EvictArgs& a, int b, int h, int slice, int kept, char* stage) {
+    const View& s = a.s;
+    const int kslices = (s.d * s.esize + kMoveSlice - 1) / kMoveSlice;
+    const bool key = slice < kslices;
+    const int off = (key ? slice : slice - kslices) * kMoveSlice, row_bytes = (key ? s.d : s.dv) * s.esize;
+    const int ch = min(kMoveSlice, row_bytes - off) / 16;
+    char* pool = (key ? a.kp + h * s.k_head : a.vp + h * s.v_head) + off;
+    const int64_t page_st = key ? s.k_page : s.v_page, token_st = key ? s.k_token : s.v_token;
+    const int32_t* table = s.table + (int64_t)b * s.max_pages;
+    const int32_t* idx = a.idx + ((int64_t)b * s.hkv + h) * a.keep;
+    constexpr int kRows = kMoveBytes / kMoveSlice;
+    const int piece = threadIdx.x & 3;      // a thread's 16 bytes of the slice
+    for (int j0 = 0; j0 < kept; j0 += kRows) {
+        const int n = min(kRows, kept - j0);
+        if (piece < ch)
+#pragma unroll 4
+            for (int j = threadIdx.x >> 2; j < n; j += kMoveThreads / 4) {
+                const int at = idx[j0 + j], tp = at / s.page;
+                cp_async16((uint32_t)__cvta_generic_to_shared(stage + j * kMoveSlice + piece * 16),
+                           pool + table[tp] * page_st + (at - tp * s.page) * token_st + piece * 16, true);
+            }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        if (piece < ch)
+            for (int j = threadIdx.x >> 2; j < n; j += kMoveThreads / 4) {
+                const int at = j0 + j, tp = at / s.page;
+                *reinterpret_cast<uint4*>(pool + table[tp] * page_st + (at - tp * s.page) * token_st + piece * 16) =
+                    *reinterpret_cast<const uint4*>(stage + j * kMoveSlice + piece * 16);
+            }
+        __syncthreads();
+    }
+}
+
+// Moves the kept rows and their scores.  blockIdx.z = sequence, y = kv head;
+// x = 0 takes the scores, the others the rows: in place a slice each, into
+// other pages 128 rows each (a warp 16 of them), where the order is free.
+__global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArgs a) {
+    extern __shared__ __align__(16) char stage[];
+    grid_dependency_wait();
+    const View& s = a.s;
+    const int h = blockIdx.y, b = blockIdx.z, part = blockIdx.x;
+    const int len = a.ws_lens[2 * b], kept = a.ws_lens[2 * b + 1];
+    constexpr int kBlockRows = kMoveThreads / 32 * kCopyRows;
+    if (part > 0 && (a.into ? (part - 1) * kBlockRows >= kept : len <= kept)) return;
+    const bool no = refused(a, b, len, kept);
+    if (part == 0) {
+        move_scores(a, b, h, len, kept, no, stage);
+        return;
+    }
+    if (no) return;
+    if (!a.into) {
+        move_in_place(a, b, h, part - 1, kept, stage);
+        return;
+    }
+    const int lane = threadIdx.x & 31, j = (part - 1) * kBlockRows + (threadIdx.x >> 5) * kCopyRows + lane;
+    RowCopy r{nullptr, nullptr, nullptr, nullptr, false};
+    if (lane < kCopyRows && j < kept) {
+        const int at = a.idx[((int64_t)b * s.hkv + h) * a.keep + j], tp = at / s.page, slot = at - tp * s.page;
+        const int to = j / s.page, to_slot = j - to * s.page;
+        const int64_t from_page = s.table[(int64_t)b * s.max_pages + tp], to_page = a.into[(int64_t)b * s.max_pages + to];
+        r.ks = a.kp + from_page * s.k_page + h * s.k_head + slot * s.k_token;
+        r.vs = a.vp + from_page * s.v_page + h * s.v_head + slot * s.v_token;
+        r.kd = a.kp + to_page * s.k_page + h * s.k_head + to_slot * s.k_token;
+        r.vd = a.vp + to_page * s.v_page + h * s.v_head + to_slot * s.v_token;
+        r.ok = true;
+    }
+    copy_rows(r, s.d * s.esize / 16, s.dv * s.esize / 16);
+}
+
+// The two kernels' shared-memory limits, once per device.
+wc_status evict_setup() {
+    static std::atomic<uint64_t> done{0};   // a bit per device number (the first 64; the others set it each time)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WC_ERR_CUDA;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return WC_OK;
+    if (cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectHeld * 4) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(cache_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes) != cudaSuccess)
+        return WC_ERR_CUDA;
+    if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return WC_OK;
+}
+
 wc_status launch_evict(const EvictArgs& a, cudaStream_t st) {
     const View& s = a.s;
+    wc_status e = evict_setup();
+    if (e != WC_OK) return e;
     if (cudaMemsetAsync(a.marks, 0, sizeof(int32_t) * (size_t)s.n_pages, st) != cudaSuccess) return WC_ERR_CUDA;
-    const int per = (s.max_pages + 255) / 256;
-    cache_mark_kernel<<<dim3(per < 32 ? per : 32, s.B), 256, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
-    cache_select_kernel<<<s.B * s.hkv, kSelectThreads, 0, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
-    if (cudaFuncSetAttribute(cache_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes) != cudaSuccess)
-        return WC_ERR_CUDA;
-    cache_move_kernel<<<dim3(s.hkv, s.B, 3), kMoveThreads, kMoveBytes, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? WC_OK : WC_ERR_CUDA;
+    // blocks of one (sequence, kv head): one for each kSelectSlice positions, while they leave no SM without a unit
+    const int64_t units = (int64_t)s.B * s.hkv;
+    int ranks = 1;
+    while (ranks < kSelectCluster && 2 * ranks * units <= 2 * 148 && (int64_t)ranks * kSelectSlice < s.cap) ranks *= 2;
+    if (units * ranks > INT32_MAX || s.hkv > 65535) return WC_ERR_UNSUPPORTED;
+    const int per = ((s.cap + ranks - 1) / ranks + 31) / 32 * 32;
+    const int held = per < kSelectHeld ? per : kSelectHeld;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(units * ranks));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = (size_t)held * 4;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, cache_select_kernel, a, held) != cudaSuccess) return WC_ERR_CUDA;
+    const int slices = (s.d * s.esize + kMoveSlice - 1) / kMoveSlice + (s.dv * s.esize + kMoveSlice - 1) / kMoveSlice;
+    const int rows = kMoveThreads / 32 * kCopyRows;
+    at = cudaLaunchAttribute{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(1 + (a.into ? (a.keep + rows - 1) / rows : slices), s.hkv, s.B);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = kMoveBytes;
+    return cudaLaunchKernelEx(&cfg, cache_move_kernel, a) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
 }
 
 struct NvtxRange {
@@ -419,9 +615,9 @@ wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const
     a.kp = static_cast<char*>(k); a.vp = static_cast<char*>(v);
     a.scores = scores; a.t = t;
     a.status = static_cast<int*>(ws);
-    const int64_t rows = (int64_t)a.s.B * t * a.s.hkv, per = kAppendThreads / 32;
-    const int64_t grid = (rows + per - 1) / per;
-    cache_append_kernel<<<(unsigned)(grid < 148 * 64 ? grid : 148 * 64), kAppendThreads, 0,
+    const int64_t items = (int64_t)a.s.B * a.s.hkv * ((t + (int64_t)kCopyRows - 1) / kCopyRows);
+    const int64_t grid = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+    cache_append_kernel<<<(unsigned)(grid < 148 * 64 ? grid : 148 * 64), kCopyThreads, 0,
                           static_cast<cudaStream_t>(stream)>>>(a);
     return cudaGetLastError() == cudaSuccess ? WC_OK : WC_ERR_CUDA;
 }
@@ -452,6 +648,7 @@ wc_status wc_cache_attend(const wc_cache* cache, const void* Q, int64_t q_batch,
     a.cparts = reinterpret_cast<float*>(w + L.cparts);
     a.logits = scores ? reinterpret_cast<float*>(w + L.logits) : nullptr;
     a.status = static_cast<int*>(ws);
+    a.q_pairs = aligned(Q, 2 * a.s.esize) && q_batch % 2 == 0 && q_head % 2 == 0;
     a.rows = rows_of(a.s);
     a.row_tiles = (a.s.group + a.rows - 1) / a.rows;
     if (r > 0) {

@@ -216,19 +216,44 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int g0,
     }
 }
 
+// Shared memory of one coreset block, in bytes: two stages a warp of NT keys
+// and their rows of W (as they lie in memory, dv + 1 values each).  The warps'
+// sums go where the stages were.
+template <int NT, int RG>
+struct CoresetSmem {
+    int k_row, w_row, w, stage, q, p, total;
+    __host__ __device__ CoresetSmem(int d, int dv, int esize) {
+        k_row = d * esize;
+        if ((k_row / 16) % 2 == 0) k_row += 16;
+        w_row = (dv + 1) * 4;
+        w = NT * k_row;
+        stage = (w + NT * w_row + 15) / 16 * 16;
+        const int stages = kWarps * 2 * stage, merge = kWarps * RG * (dv + 2) * 4;
+        q = ((stages > merge ? stages : merge) + 15) / 16 * 16;
+        p = q + RG * d * 4;
+        total = p + kWarps * NT * RG * 4;
+    }
+};
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // One block of the coreset's share: rows [first, last) of unit (b, h)'s
-// coreset against RG query rows.  W is fp32 with a row of dv + 1 values, so its
-// rows are read in place, 4 bytes a lane; the row's last value is its weight
-// in the normaliser.
-template <typename T, int RG, int NT>
+// coreset against RG query rows, NT at a time for each warp.  W is fp32 with
+// rows of dv + 1 values (no 16-byte alignment), so a step's rows, which lie
+// side by side, come in by 4-byte asynchronous copies while the step before is
+// summed; a lane holds columns lane, lane + 32, ... and the row's last value is
+// its weight in the normaliser.  Sums in fp32 on CUDA cores: W's values cancel
+// one another, and there are few rows.
+template <typename T, int RG, int NT, int COLS>
 __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
     const View& s = a.s;
-    const SimtSmem<NT, RG> L(s.d, s.dv, sizeof(T));
+    const CoresetSmem<NT, RG> L(s.d, s.dv, sizeof(T));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* q = reinterpret_cast<float*>(smem + L.q);
     float* p = reinterpret_cast<float*>(smem + L.p) + warp * NT * RG;
-    float* merge = reinterpret_cast<float*>(smem + L.merge);
-    char* krows = smem + warp * L.warp;
+    char* stages = smem + warp * 2 * L.stage;
     const int split = index % a.csplits, unit = index / a.csplits;
     const int rt = unit % a.row_tiles, h = unit / a.row_tiles % s.hkv, b = unit / a.row_tiles / s.hkv;
     const int rows = min(a.rows, s.group - rt * a.rows);
@@ -238,36 +263,48 @@ __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
         n = n < 0 ? 0 : a.r;
     }
     const int first = split * a.csplit_len, last = min(first + a.csplit_len, n);
+    const int64_t base = ((int64_t)b * s.hkv + h) * a.r;
+    const int ck = s.d * (int)sizeof(T) / 16;
+    auto load = [&](int stage, int at) {
+        const int live = min(NT, last - at);
+        if (live > 0) {
+            const uint32_t kd = (uint32_t)__cvta_generic_to_shared(stages + stage * L.stage), wd = kd + L.w;
+            const char* k = static_cast<const char*>(a.Ks) + (base + at) * s.d * (int64_t)sizeof(T);
+            int row = lane / ck, c = lane - row * ck;
+            for (int i = lane; i < NT * ck; i += 32) {
+                cp_async16(kd + row * L.k_row + c * 16, k + (row < live ? i : 0) * 16, row < live);
+                for (c += 32; c >= ck; c -= ck) ++row;
+            }
+            const float* w = a.W + (base + at) * (s.dv + 1);
+            for (int i = lane; i < live * (s.dv + 1); i += 32) cp_async4(wd + i * 4, w + i);
+        }
+        cp_async_commit();
+    };
+    int at = first + warp * NT;
+    load(0, at);
     load_queries<T, RG>(a, b, h * s.group + rt * a.rows, rows, q);
     __syncthreads();
-    constexpr int kMaxCols = 8;   // dv <= 256: at most 8 columns a lane
-    float m[RG], l[RG], o[RG][kMaxCols];
+    float m[RG], l[RG], o[RG][COLS];
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
         m[g] = -CUDART_INF_F;
         l[g] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kMaxCols; ++i) o[g][i] = 0.f;
+        for (int i = 0; i < COLS; ++i) o[g][i] = 0.f;
     }
-    const int64_t base = ((int64_t)b * s.hkv + h) * a.r;
-    const int ck = s.d * (int)sizeof(T) / 16;
-    for (int at = first + warp * NT; at < last; at += kWarps * NT) {
+    for (int stage = 0; at < last; at += kWarps * NT, stage ^= 1) {
+        load(stage ^ 1, at + kWarps * NT);
+        cp_async_wait<1>();
         __syncwarp();
-        for (int i = lane; i < NT * ck; i += 32) {
-            const int row = i / ck, c = i - row * ck;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (at + row < last)
-                v = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(a.Ks) +
-                                                         (base + at + row) * s.d * (int64_t)sizeof(T)) + c);
-            *reinterpret_cast<uint4*>(krows + row * L.k_row + c * 16) = v;
-        }
-        __syncwarp();
+        const char* krows = stages + stage * L.stage;
+        const float* wrows = reinterpret_cast<const float*>(krows + L.w);
         float x[RG];
         tile_logits<T, RG, NT>(krows, L.k_row, q, s.d, x);
-        const int key = lane % NT;
+        const int key = lane % NT, live = min(NT, last - at);
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
-            float v = at + key < last ? x[g] : -CUDART_INF_F, top = v;
+            const float v = key < live ? x[g] : -CUDART_INF_F;
+            float top = v;
 #pragma unroll
             for (int e = 1; e < NT; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
             if (top > m[g]) {
@@ -275,34 +312,39 @@ __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
                 m[g] = top;
                 l[g] *= f;
 #pragma unroll
-                for (int i = 0; i < kMaxCols; ++i) o[g][i] *= f;
+                for (int i = 0; i < COLS; ++i) o[g][i] *= f;
             }
             const float w = ex2(v - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
             if (lane < NT) p[key * RG + g] = w;
         }
         __syncwarp();
-        const int live = min(NT, last - at);
+#pragma unroll 2
         for (int j = 0; j < live; ++j) {
-            const float* w = a.W + (base + at + j) * (s.dv + 1);
-            float y[kMaxCols];
+            const float* w = wrows + j * (s.dv + 1);
+            float y[COLS], e[RG];
 #pragma unroll
-            for (int i = 0; i < kMaxCols; ++i) y[i] = lane + 32 * i < s.dv ? __ldg(w + lane + 32 * i) : 0.f;
-            const float z = __ldg(w + s.dv);
+            for (int i = 0; i < COLS; ++i) y[i] = lane + 32 * i < s.dv ? w[lane + 32 * i] : 0.f;
+            const float z = w[s.dv];
+#pragma unroll
+            for (int g = 0; g < RG; ++g) e[g] = p[j * RG + g];
 #pragma unroll
             for (int g = 0; g < RG; ++g) {
-                const float e = p[j * RG + g];
-                l[g] = fmaf(e, z, l[g]);
+                l[g] = fmaf(e[g], z, l[g]);
 #pragma unroll
-                for (int i = 0; i < kMaxCols; ++i) o[g][i] = fmaf(e, y[i], o[g][i]);
+                for (int i = 0; i < COLS; ++i) o[g][i] = fmaf(e[g], y[i], o[g][i]);
             }
         }
+        __syncwarp();
     }
+    cp_async_wait<0>();
+    __syncthreads();
+    float* merge = reinterpret_cast<float*>(smem);
     const int ld = s.dv + 2;
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
         float* row = merge + (warp * RG + g) * ld;
 #pragma unroll
-        for (int i = 0; i < kMaxCols; ++i)
+        for (int i = 0; i < COLS; ++i)
             if (lane + 32 * i < s.dv) row[lane + 32 * i] = o[g][i];
         if (lane == 0) {
             row[s.dv] = m[g];
@@ -326,7 +368,7 @@ __global__ void __launch_bounds__(kThreads) cache_attend_simt_kernel(const Atten
     const View& s = a.s;
     const int blocks = a.blocks;
     if ((int)blockIdx.x >= blocks) {
-        coreset_block<T, RG, NT>(a, blockIdx.x - blocks, smem);
+        coreset_block<T, RG, NT, NVI * 4>(a, blockIdx.x - blocks, smem);
         return;
     }
     constexpr int kTile = kWarps * NT;
@@ -508,8 +550,17 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t t[3]) {
     }
 }
 
+// (x, y) += (u, v) as one packed fp32 addition.
+__device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(u), "f"(v));
+}
+
 constexpr int kMmaKeys = 16;     // keys of one warp's step
 constexpr int kMmaStages = 3;
+template <int DP> constexpr int kCoresetKeys = DP > 128 ? 8 : 16;   // (two stages of wider rows leave too little room)
 
 // bf16 pages on tensor cores (mma.sync: a group's 1 to 16 query rows fill one
 // 16-row tile at most, and the pass is bound by the bytes of the keys and
@@ -539,7 +590,7 @@ __global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const Attend
     const View& s = a.s;
     const int blocks = a.blocks;
     if ((int)blockIdx.x >= blocks) {
-        coreset_block<bf16, kRows, 16>(a, blockIdx.x - blocks, smem);
+        coreset_block<bf16, kRows, kCoresetKeys<DP>, DP / 32>(a, blockIdx.x - blocks, smem);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -565,32 +616,6 @@ __global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const Attend
         const int rows = min(a.rows, s.group - rt * a.rows), g0 = h * s.group + rt * a.rows;
         const char* kh = a.kp + h * s.k_head;
         const char* vh = a.vp + h * s.v_head;
-        // Query fragments, as they are (the logits are scaled in fp32): rows
-        // quad and, where the rows are not copies, quad + 8.
-        uint32_t q[DP / 16][SETS == 3 ? 4 : 2];
-        {
-            const bf16* src = static_cast<const bf16*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
-            auto two = [&](int row, int col) {
-                uint32_t v = 0;
-                if (row < rows && col < s.d) {
-                    const bf16* p = src + row * a.q_head + col;
-                    v = (uint32_t)__bfloat16_as_ushort(p[0]) | (uint32_t)__bfloat16_as_ushort(p[1]) << 16;
-                }
-                return v;
-            };
-            const int r0 = quad % kRows;
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                const int col = k * 16 + pair * 2;
-                if (SETS == 3) {
-                    q[k][0] = two(quad, col); q[k][1] = two(quad + 8, col);
-                    q[k][SETS == 3 ? 2 : 0] = two(quad, col + 8); q[k][SETS == 3 ? 3 : 1] = two(quad + 8, col + 8);
-                } else {
-                    q[k][0] = two(r0, col);
-                    q[k][1] = two(r0, col + 8);
-                }
-            }
-        }
         float o[DP / 8][4];
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n)
@@ -653,6 +678,33 @@ __global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const Attend
             cp_async_commit();
         }
         next = locate(k0 + kMmaStages - 1);
+        // Query fragments, as they are (the logits are scaled in fp32): rows
+        // quad and, where the rows are not copies, quad + 8.
+        uint32_t q[DP / 16][SETS == 3 ? 4 : 2];
+        {
+            const bf16* src = static_cast<const bf16*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
+            auto two = [&](int row, int col) {
+                uint32_t v = 0;
+                if (row < rows && col < s.d) {
+                    const bf16* p = src + row * a.q_head + col;
+                    if (a.q_pairs) v = *reinterpret_cast<const uint32_t*>(p);
+                    else v = (uint32_t)__bfloat16_as_ushort(p[0]) | (uint32_t)__bfloat16_as_ushort(p[1]) << 16;
+                }
+                return v;
+            };
+            const int r0 = quad % kRows;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                const int col = k * 16 + pair * 2;
+                if (SETS == 3) {
+                    q[k][0] = two(quad, col); q[k][1] = two(quad + 8, col);
+                    q[k][SETS == 3 ? 2 : 0] = two(quad, col + 8); q[k][SETS == 3 ? 3 : 1] = two(quad + 8, col + 8);
+                } else {
+                    q[k][0] = two(r0, col);
+                    q[k][1] = two(r0, col + 8);
+                }
+            }
+        }
         int stage = 0;
         for (int i = k0; i < k1; ++i) {
             cp_async_wait<kMmaStages - 2>();
@@ -774,8 +826,8 @@ __global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const Attend
                             mma16816(z, w[0][0][1], w[kMine - 1][0][1], w[0][1][1], w[kMine - 1][1][1], b0, b1);
                             mma16816(z, w[0][0][2], w[kMine - 1][0][2], w[0][1][2], w[kMine - 1][1][2], b0, b1);
                         }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[2 * n + u][e] += z[e];
+                        add2(o[2 * n + u][0], o[2 * n + u][1], z[0], z[1]);
+                        add2(o[2 * n + u][2], o[2 * n + u][3], z[2], z[3]);
                     }
                 }
             }
@@ -828,93 +880,130 @@ __global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const Attend
 }
 
 // Joins the partial rows of every query row, and adds the step's weights to
-// the scores.  Blocks [0, B hq) take a query row each; with scores, the others
-// take kScoreKeys positions of one (sequence, kv head) each.
+// the scores.  Blocks [0, B hq) take a query row each: a warp takes every
+// fourth set, a lane four columns.  With scores, the others take kScoreKeys
+// positions of one (sequence, kv head) each: the rows' references and
+// normalisers first (a warp a row), then the logits that the pages' kernel
+// left, 2^(x - m) / L summed over the group's rows.
 constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kScoreKeys = 1024;
-
-struct Parts {
-    const float* p; int n; int64_t step;   // sets of the pages' share, one per block
-    const float* c; int nc; int64_t cstep; // sets of the coreset's share
-};
+constexpr int kScoreRows = 64;    // rows whose references are held at a time
 
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendArgs a, int tile) {
-    __shared__ int64_t place_sh[4 + kJoinThreads / 32];
-    __shared__ float red[kJoinThreads / 32][2];
+    __shared__ int64_t place_sh[4 + kJoinWarps];
+    __shared__ float sums[kJoinWarps][256];
+    __shared__ float refs[kScoreRows][2];
     const View& s = a.s;
     const int per_tile = s.hkv * a.row_tiles, dv = s.dv, ld = c1_row(dv);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool score = (int)blockIdx.x >= s.B * s.hq;
     const int chunks = (s.cap + kScoreKeys - 1) / kScoreKeys;
-    int b, hq0, n_rows, key0 = 0;
+    int b, hq0, key0 = 0;
     if (!score) {
         b = blockIdx.x / s.hq;
         hq0 = blockIdx.x % s.hq;
-        n_rows = 1;
     } else {
         const int i = blockIdx.x - s.B * s.hq;
         b = i / chunks / s.hkv;
         hq0 = i / chunks % s.hkv * s.group;
         key0 = i % chunks * kScoreKeys;
-        n_rows = s.group;
     }
     const int len = checked_len(a.lens, b, s.cap, a.status);
     if (score && key0 >= len) return;
     grid_dependency_wait();   // the partial rows (and everything before them) are there from here on
     const Place at = find_place<kJoinThreads>(s, a.lens, tile, per_tile, 0, a.blocks, b, a.status, place_sh);
     const int tiles = (len + tile - 1) / tile;
-    float acc[kScoreKeys / kJoinThreads];
-#pragma unroll
-    for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) acc[i] = 0.f;
-    for (int r = 0; r < n_rows; ++r) {
-        const int g = (hq0 + r) % s.group, in_b = (hq0 + r) / s.group * a.row_tiles + g / a.rows;
-        const int in_unit = g % a.rows;
-        Parts ps{nullptr, 0, (int64_t)a.rows * ld, nullptr, 0, (int64_t)a.rows * ld};
+    // sets of partial rows of query row hq: first of the pages' (one per block), then of the coreset's
+    const float *pages = nullptr, *core = nullptr;
+    int n_pages = 0, n = 0;
+    const int64_t step = (int64_t)a.rows * ld;
+    auto find_sets = [&](int hq) {
+        const int g = hq % s.group, in_b = hq / s.group * a.row_tiles + g / a.rows, in_unit = g % a.rows;
+        n_pages = 0;
         if (tiles > 0) {
             const int64_t t0 = at.before + (int64_t)in_b * tiles;
             const int c0 = block_of(t0, at.total, at.blocks), c1 = block_of(t0 + tiles - 1, at.total, at.blocks);
-            if (c0 == c1 && !a.csplits && !a.logits) return;   // finished by the block itself
-            ps.p = a.parts + ((int64_t)b * per_tile + in_b + c0) * ps.step + in_unit * ld;
-            ps.n = c1 - c0 + 1;
+            if (c0 == c1 && !a.csplits && !a.logits) return false;   // finished by the block itself
+            pages = a.parts + ((int64_t)b * per_tile + in_b + c0) * step + in_unit * ld;
+            n_pages = c1 - c0 + 1;
         }
-        if (a.csplits) {
-            ps.c = a.cparts + ((int64_t)b * per_tile + in_b) * a.csplits * ps.cstep + in_unit * ld;
-            ps.nc = a.csplits;
-        }
-        const int n = ps.n + ps.nc;
-        auto set = [&](int i) { return i < ps.n ? ps.p + i * ps.step : ps.c + (i - ps.n) * ps.cstep; };
-        // the maximum and the normaliser over all sets (fixed order: by set within a thread, then by thread)
-        float m = -CUDART_INF_F;
-        for (int i = threadIdx.x; i < n; i += kJoinThreads) m = fmaxf(m, set(i)[dv + 1]);
+        if (a.csplits) core = a.cparts + ((int64_t)b * per_tile + in_b) * a.csplits * step + in_unit * ld;
+        n = n_pages + a.csplits;
+        return true;
+    };
+    auto set = [&](int i) { return i < n_pages ? pages + i * step : core + (i - n_pages) * step; };
+    // a warp's reference and normaliser over all sets, in an order that the number of sets alone decides
+    auto total = [&](float& m, float& l) {
+        m = -CUDART_INF_F;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, set(i)[dv + 1]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][0] = m;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w][0]);
         const float ref = m == -CUDART_INF_F ? 0.f : m;
-        float l = 0.f;
-        for (int i = threadIdx.x; i < n; i += kJoinThreads) l += ex2(set(i)[dv + 1] - ref) * set(i)[dv];
+        l = 0.f;
+        for (int i = lane; i < n; i += 32) l = fmaf(ex2(set(i)[dv + 1] - ref), set(i)[dv], l);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][1] = l;
-        __syncthreads();
-        l = 0.f;
+    };
+    if (!score) {
+        if (!find_sets(hq0)) return;
+        float m, l;
+        total(m, l);
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        float o[2][4];
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w][1];
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
+#pragma unroll 4
+        for (int i = warp; i < n; i += kJoinWarps) {
+            const float* p = set(i);
+            const float f = ex2(p[dv + 1] - ref);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (k * 128 + lane * 4 < dv) {
+                    const float4 v = *reinterpret_cast<const float4*>(p + k * 128 + lane * 4);
+                    o[k][0] = fmaf(f, v.x, o[k][0]);
+                    o[k][1] = fmaf(f, v.y, o[k][1]);
+                    o[k][2] = fmaf(f, v.z, o[k][2]);
+                    o[k][3] = fmaf(f, v.w, o[k][3]);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (k * 128 + lane * 4 < dv)
+                *reinterpret_cast<float4*>(&sums[warp][k * 128 + lane * 4]) = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
         __syncthreads();
+        const int64_t row = (int64_t)b * s.hq + hq0;
         const bool empty = nothing(m, l);
-        if (!score) {
-            const int64_t row = (int64_t)b * s.hq + hq0;
-            for (int c = threadIdx.x; c < dv; c += kJoinThreads) {
-                float o = 0.f;
-                for (int i = 0; i < n; ++i) o = fmaf(ex2(set(i)[dv + 1] - ref), set(i)[c], o);
-                a.out[row * dv + c] = empty ? 0.f : o / l;
+        for (int c = threadIdx.x; c < dv; c += kJoinThreads) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) v += sums[w][c];
+            a.out[row * dv + c] = empty ? 0.f : v / l;
+        }
+        if (threadIdx.x == 0 && a.lse) a.lse[row] = log_sum(m, l);
+        return;
+    }
+    float acc[kScoreKeys / kJoinThreads];
+#pragma unroll
+    for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) acc[i] = 0.f;
+    for (int r0 = 0; r0 < s.group; r0 += kScoreRows) {
+        const int rows = min(kScoreRows, s.group - r0);
+        __syncthreads();
+        for (int r = warp; r < rows; r += kJoinWarps) {
+            find_sets(hq0 + r0 + r);
+            float m, l;
+            total(m, l);
+            if (lane == 0) {
+                refs[r][0] = m == -CUDART_INF_F ? 0.f : m;
+                refs[r][1] = nothing(m, l) ? 0.f : 1.f / l;   // no weight anywhere: 0 for every key
             }
-            if (threadIdx.x == 0 && a.lse)
-                a.lse[row] = log_sum(m, l);
-        } else if (!empty) {
-            const float* x = a.logits + ((int64_t)b * s.hq + hq0 + r) * s.cap;
-            const float inv = 1.f / l;
+        }
+        __syncthreads();
+        for (int r = 0; r < rows; ++r) {
+            const float* x = a.logits + ((int64_t)b * s.hq + hq0 + r0 + r) * s.cap;
+            const float ref = refs[r][0], inv = refs[r][1];
 #pragma unroll
             for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) {
                 const int key = key0 + i * kJoinThreads + threadIdx.x;
@@ -922,13 +1011,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
             }
         }
     }
-    if (score) {
-        float* out = a.scores + ((int64_t)b * s.hkv + hq0 / s.group) * s.cap;
+    float* out = a.scores + ((int64_t)b * s.hkv + hq0 / s.group) * s.cap;
 #pragma unroll
-        for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) {
-            const int key = key0 + i * kJoinThreads + threadIdx.x;
-            if (key < len) out[key] += acc[i];
-        }
+    for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) {
+        const int key = key0 + i * kJoinThreads + threadIdx.x;
+        if (key < len) out[key] += acc[i];
     }
 }
 
@@ -1001,7 +1088,8 @@ wc_status run(AttendArgs a, void (*kern)(const AttendArgs), int smem, int tile, 
 
 template <int RG, int NT>
 wc_status run_simt(const AttendArgs& a, cudaStream_t st) {
-    const int smem = SimtSmem<NT, RG>(a.s.d, a.s.dv, 4).total;
+    int smem = SimtSmem<NT, RG>(a.s.d, a.s.dv, 4).total;
+    if (a.csplits) smem = max(smem, CoresetSmem<NT, RG>(a.s.d, a.s.dv, 4).total);
     return a.s.dv <= 128 ? run(a, cache_attend_simt_kernel<RG, NT, 1>, smem, kWarps * NT, st)
                          : run(a, cache_attend_simt_kernel<RG, NT, 2>, smem, kWarps * NT, st);
 }
@@ -1016,7 +1104,7 @@ template <int DP, int SETS>
 wc_status run_mma(const AttendArgs& a, cudaStream_t st) {
     constexpr int rows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
     int smem = kWarps * kMmaStages * 2 * kMmaKeys * DP * 2;
-    if (a.csplits) smem = max(smem, SimtSmem<16, rows>(a.s.d, a.s.dv, 2).total);
+    if (a.csplits) smem = max(smem, CoresetSmem<kCoresetKeys<DP>, rows>(a.s.d, a.s.dv, 2).total);
     return run(a, cache_attend_mma_kernel<DP, SETS>, smem, kWarps * kMmaKeys, st);
 }
 

@@ -42,6 +42,7 @@ Layout make_layout(const View& s, bool accumulate);
 struct AttendArgs {
     View s;
     const void* Q; int64_t q_batch, q_head;      // strides in elements
+    bool q_pairs;                                // pairs of a row's elements are aligned together
     const char* kp; const char* vp;
     const int32_t* lens;
     const void* Ks; const float* W; const int32_t* rank; int r;   // coreset, or r = 0
