@@ -38,6 +38,12 @@ wc_status make_view(const wc_cache* in, View* o) {
     o->B = c.batch; o->hq = c.hq; o->hkv = c.hkv; o->group = c.hq / c.hkv;
     o->d = c.d; o->dv = c.dv;
     o->page = c.page; o->n_pages = c.n_pages; o->max_pages = c.max_pages; o->cap = c.max_pages * c.page;
+    // m = floor(2^(31+s) / page) + 1 with 2^(s-1) < page <= 2^s: m page - 2^(31+s) <= page <= 2^s, so the
+    // product is off by less than one part in 2^31 and the quotient exact below 2^31
+    int sh = 0;
+    while ((1 << sh) < c.page) ++sh;
+    o->page_mul = (uint32_t)((1ull << (31 + sh)) / (uint64_t)c.page + 1);
+    o->page_shift = 31 + sh;
     o->dtype = c.dtype; o->esize = c.dtype == WC_BF16 ? 2 : 4;
     o->beta = c.scale > 0.f ? (double)c.scale : 1.0 / sqrt((double)c.d);
     o->table = nullptr;
@@ -78,12 +84,14 @@ Layout make_layout(const View& s, bool accumulate) {
         return at;
     };
     const int rows = rows_of(s), tiles = (s.group + rows - 1) / rows;
-    const size_t units = (size_t)s.B * s.hkv * tiles, set = sizeof(float) * rows * c1_row(s.dv);
+    const size_t units = (size_t)s.B * s.hkv * tiles, set = sizeof(float) * rows * s.dv, lm = sizeof(float2) * rows;
     L.status = take(256);
     L.marks = take(sizeof(int32_t) * (size_t)s.n_pages);
     L.lens = take(sizeof(int32_t) * 2 * (size_t)s.B);
-    L.parts = take((units + kMaxBlocks) * set);
+    L.parts = take((units + kMaxWorkers) * set);
+    L.parts_lm = take((units + kMaxWorkers) * lm);
     L.cparts = take((units + kCoresetBlocks) * set);
+    L.cparts_lm = take((units + kCoresetBlocks) * lm);
     L.logits = take(accumulate ? sizeof(float) * (size_t)s.B * s.hq * s.cap : 0);
     L.end = off;
     return L;
@@ -113,10 +121,6 @@ struct RowCopy {
     char *kd, *vd;
     bool ok;
 };
-
-__device__ __forceinline__ const char* shfl_ptr(const char* p, int from) {
-    return reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), from));
-}
 
 // One warp copies 16 key rows and 16 value rows in 16-byte pieces, four pieces a
 // lane in flight; rows that are not `ok` are skipped.  A copy, bound by the
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_append_kernel(const Append
             if (at < 0 || at >= s.cap) {
                 record_status(a.status, WC_ERR_BOUNDS);
             } else {
-                const int tp = (int)at / s.page, slot = (int)at - tp * s.page;
+                const int tp = page_of(s, (int)at), slot = (int)at - tp * s.page;
                 const int pg = checked_page(s, s.table, b, tp, a.status);
                 if (pg >= 0) {
                     r.ks = a.K + b * a.k_batch + h * a.k_head + j * a.k_row;
@@ -263,7 +267,7 @@ __device__ __forceinline__ int block_scan(int v, int* sh) {
 // real caches.
 __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const EvictArgs a, int held) {
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ int hist[3][2048];
+    __shared__ __align__(16) int hist[3][2048];   // (read two at a time)
     __shared__ int sh[kSelectWarps];
     __shared__ int counts[kSelectWarps][2];
     __shared__ int block_counts[2];
@@ -462,16 +466,16 @@ __device__ void move_in_place(const EvictArgs& a, int b, int h, int slice, int k
         if (piece < ch)
 #pragma unroll 4
             for (int j = threadIdx.x >> 2; j < n; j += kMoveThreads / 4) {
-                const int at = idx[j0 + j], tp = at / s.page;
+                const int at = idx[j0 + j], tp = page_of(s, at);
                 cp_async16((uint32_t)__cvta_generic_to_shared(stage + j * kMoveSlice + piece * 16),
-                           pool + table[tp] * page_st + (at - tp * s.page) * token_st + piece * 16, true);
+                           pool + table[tp] * page_st + (at - tp * s.page) * token_st + piece * 16);
             }
         cp_async_commit();
         cp_async_wait<0>();
         __syncthreads();
         if (piece < ch)
             for (int j = threadIdx.x >> 2; j < n; j += kMoveThreads / 4) {
-                const int at = j0 + j, tp = at / s.page;
+                const int at = j0 + j, tp = page_of(s, at);
                 *reinterpret_cast<uint4*>(pool + table[tp] * page_st + (at - tp * s.page) * token_st + piece * 16) =
                     *reinterpret_cast<const uint4*>(stage + j * kMoveSlice + piece * 16);
             }
@@ -503,8 +507,8 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArg
     const int lane = threadIdx.x & 31, j = (part - 1) * kBlockRows + (threadIdx.x >> 5) * kCopyRows + lane;
     RowCopy r{nullptr, nullptr, nullptr, nullptr, false};
     if (lane < kCopyRows && j < kept) {
-        const int at = a.idx[((int64_t)b * s.hkv + h) * a.keep + j], tp = at / s.page, slot = at - tp * s.page;
-        const int to = j / s.page, to_slot = j - to * s.page;
+        const int at = a.idx[((int64_t)b * s.hkv + h) * a.keep + j], tp = page_of(s, at), slot = at - tp * s.page;
+        const int to = page_of(s, j), to_slot = j - to * s.page;
         const int64_t from_page = s.table[(int64_t)b * s.max_pages + tp], to_page = a.into[(int64_t)b * s.max_pages + to];
         r.ks = a.kp + from_page * s.k_page + h * s.k_head + slot * s.k_token;
         r.vs = a.vp + from_page * s.v_page + h * s.v_head + slot * s.v_token;
@@ -646,6 +650,8 @@ wc_status wc_cache_attend(const wc_cache* cache, const void* Q, int64_t q_batch,
     a.out = out; a.lse = lse; a.scores = scores;
     a.parts = reinterpret_cast<float*>(w + L.parts);
     a.cparts = reinterpret_cast<float*>(w + L.cparts);
+    a.parts_lm = reinterpret_cast<float2*>(w + L.parts_lm);
+    a.cparts_lm = reinterpret_cast<float2*>(w + L.cparts_lm);
     a.logits = scores ? reinterpret_cast<float*>(w + L.logits) : nullptr;
     a.status = static_cast<int*>(ws);
     a.q_pairs = aligned(Q, 2 * a.s.esize) && q_batch % 2 == 0 && q_head % 2 == 0;

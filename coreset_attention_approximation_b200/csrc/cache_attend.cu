@@ -5,9 +5,11 @@
 // One pass over the keys and values with a running maximum per query row (in
 // log2 units, so one multiplication by beta log2(e) is folded into the query):
 // a partial result is (O, l, m) with O = sum 2^(x - m) v, l = sum 2^(x - m).
-// The key tiles of the whole batch are divided evenly over the blocks
-// (wc_cache.cuh), whatever the lengths, and a second kernel joins a unit's
-// partial rows in order of the blocks.
+// The key tiles of the whole batch are divided evenly over the warps
+// (wc_cache.cuh), whatever the lengths; a warp streams its tiles through a ring
+// of its own in shared memory, on from one sequence or head to the next, and
+// never waits for another.  A second kernel joins a unit's partial rows in
+// order of the warps.
 #include <atomic>
 #include <mutex>
 
@@ -17,33 +19,7 @@ namespace wc {
 namespace cache {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-
-// Where a warp's 16 or 8 keys lie: lane j < NT holds key j's byte offsets.
-struct KeyPlace {
-    int64_t k, v;
-    bool valid;
-};
-
-// Shared memory of one block of the CUDA-core kernel, in bytes.
-template <int NT, int RG>
-struct SimtSmem {
-    int k_row, v_row;      // bytes of a staged row; k rows padded to an odd number of 16-byte units
-    int stage, warp;       // bytes of one stage and of one warp's stages
-    int q, p, merge, total;
-    __host__ __device__ SimtSmem(int d, int dv, int esize) {
-        k_row = d * esize;
-        if ((k_row / 16) % 2 == 0) k_row += 16;
-        v_row = dv * esize;
-        stage = NT * (k_row + v_row);
-        warp = 2 * stage;
-        q = kWarps * warp;
-        p = q + RG * d * 4;
-        merge = p + kWarps * NT * RG * 4;
-        total = merge + kWarps * RG * (dv + 2) * 4;
-    }
-};
+constexpr int kSimtWarps = 4;
 
 template <typename T> __device__ __forceinline__ void load_chunk(const char* p, float* x);
 template <> __device__ __forceinline__ void load_chunk<float>(const char* p, float* x) {
@@ -59,21 +35,6 @@ template <> __device__ __forceinline__ void load_chunk<__nv_bfloat16>(const char
         x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
 }
-// The running state of one warp: its keys' sums for RG query rows.
-template <int RG, int NVI>
-struct Running {
-    float m[RG], l[RG], o[RG][NVI * 4];   // l: this lane's share; o: this lane's columns and key group
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int g = 0; g < RG; ++g) {
-            m[g] = -CUDART_INF_F;
-            l[g] = 0.f;
-#pragma unroll
-            for (int i = 0; i < NVI * 4; ++i) o[g][i] = 0.f;
-        }
-    }
-};
-
 // Logits of NT staged keys against RG query rows: lane = (key, part of d).
 // Every lane ends with its key's whole sums.
 template <typename T, int RG, int NT>
@@ -104,61 +65,147 @@ __device__ __forceinline__ void tile_logits(const char* krows, int k_row, const 
         for (int g = 0; g < RG; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
 }
 
-// New maxima from a tile's logits (-inf where masked); rescales the state and
-// leaves the tile's weights in p (shared, [NT][RG]).
-template <int RG, int NT, int NVI>
-__device__ __forceinline__ void tile_weights(Running<RG, NVI>& st, const float s[RG], float* p) {
-    const int lane = threadIdx.x & 31, key = lane % NT, part = lane / NT;
-#pragma unroll
-    for (int g = 0; g < RG; ++g) {
-        float top = s[g];
-#pragma unroll
-        for (int o = 1; o < NT; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (top > st.m[g]) {
-            const float f = ex2(st.m[g] - top);   // 0 where nothing was summed yet
-            st.m[g] = top;
-            st.l[g] *= f;
-#pragma unroll
-            for (int i = 0; i < NVI * 4; ++i) st.o[g][i] *= f;
+// A warp's way through its tiles: the unit (sequence b, kv head h, row tile rt)
+// and the tile k of its `tiles`.
+struct Walk {
+    int left;          // tiles to go, this one included
+    int b, h, rt, k, tiles, len;
+    // first tile of worker c, from the place of a worker not behind it
+    __device__ __forceinline__ void start(const AttendArgs& a, const Place& at, int c, int tile) {
+        const Share share(at.total, max(at.workers, 1));
+        int t = c < at.workers ? share.first(c) : at.total;
+        left = c < at.workers ? share.first(c + 1) - t : 0;
+        b = h = rt = k = tiles = len = 0;
+        if (left <= 0) return;
+        const int per_tile = a.s.hkv * a.row_tiles;
+        t -= at.before;
+        for (b = at.b;; ++b) {
+            len = checked_len(a.lens, b, a.s.cap, a.status);
+            tiles = (len + tile - 1) / tile;
+            if (t < tiles * per_tile) break;
+            t -= tiles * per_tile;
         }
-        // nothing but masked keys so far: the reference is 0, every weight 2^-inf = 0
-        const float w = ex2(s[g] - (st.m[g] == -CUDART_INF_F ? 0.f : st.m[g]));
-        if (part == 0) {
-            st.l[g] += w;
-            p[key * RG + g] = w;
-        }
+        const int unit = t / tiles;
+        k = t - unit * tiles;
+        h = unit / a.row_tiles;
+        rt = unit - h * a.row_tiles;
     }
-}
+    // past n tiles of this unit, to the next unit behind its last one
+    __device__ __forceinline__ void skip(const AttendArgs& a, int n, int tile) {
+        left -= n;
+        k += n;
+        if (left <= 0 || k < tiles) return;
+        k = 0;
+        if (++rt < a.row_tiles) return;
+        rt = 0;
+        if (++h < a.s.hkv) return;
+        h = 0;
+        do len = checked_len(a.lens, ++b, a.s.cap, a.status);
+        while (len == 0);
+        tiles = (len + tile - 1) / tile;
+    }
+    __device__ __forceinline__ void next(const AttendArgs& a, int tile) { skip(a, 1, tile); }
+};
 
-// Sums a warp's state over its lanes and leaves it in shared memory:
-// [RG][dv + 2] with m and l behind the columns.
-template <int RG, int NVI>
-__device__ __forceinline__ void leave_state(Running<RG, NVI>& st, float* to, int dv, int groups) {
-    const int lane = threadIdx.x & 31, cols = 32 / groups;
-#pragma unroll
-    for (int g = 0; g < RG; ++g) {
-        float l = st.l[g];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        for (int o = cols; o < 32; o <<= 1)
-#pragma unroll
-            for (int i = 0; i < NVI * 4; ++i) st.o[g][i] += __shfl_xor_sync(0xffffffffu, st.o[g][i], o);
-        float* row = to + g * (dv + 2);
-        if (lane < cols) {
-#pragma unroll
-            for (int i = 0; i < NVI; ++i) {
-                const int c = lane + i * cols;
-                if (c < dv / 4)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) row[c * 4 + e] = st.o[g][i * 4 + e];
+// A warp's ring of stages in shared memory.  A stage holds the key rows of one
+// step's KEYS keys, then their value rows, each row 16 bytes longer than DP
+// elements, so that eight rows at one column lie in eight different bank groups.
+// Rows come by 16-byte asynchronous copies, a row to 32 lanes or fewer.  Where
+// a page holds whole steps, a lane's sources are one base and a fixed stride
+// apart, and no copy needs an address of its own beyond an addition: the
+// kernels are bound by instruction issue before they are by memory (one bulk
+// copy a row, issued lane by lane, cost 16 cycles each and 4.4 TB/s in all).
+template <int KEYS, int DP, int ESIZE, int STAGES>
+struct Ring {
+    static constexpr int kRow = DP * ESIZE + 16, kStage = 2 * KEYS * kRow;
+    static constexpr int kBytes = STAGES * kStage;
+    static constexpr int kChunks = DP * ESIZE / 16;                  // pieces of a row
+    static constexpr int kPass = kChunks < 32 ? 32 / kChunks : 1;    // rows of one warp-wide copy
+    static constexpr int kParts = kChunks < 32 ? 1 : kChunks / 32;   // copies a row takes
+    uint32_t mem;            // the ring, and this lane's piece of its first row
+    int row0, ch;            // this lane's first row of a step and its piece
+    bool whole;              // a page holds whole steps
+    const char *k, *v;       // the next step: this lane's first sources (whole), or its key's row
+    uint32_t live;           // and a bit for each of its keys that is there
+
+    __device__ __forceinline__ void init(const AttendArgs& a, char* memory) {
+        const View& s = a.s;
+        const int lane = threadIdx.x & 31;
+        row0 = lane / kChunks % kPass;
+        ch = lane % (kChunks < 32 ? kChunks : 32);
+        mem = (uint32_t)__cvta_generic_to_shared(memory) + row0 * kRow + ch * 16;
+        whole = s.page % KEYS == 0;
+        k = v = nullptr;
+        live = 0;
+        // columns past the width are never copied and count as zeros
+        if (s.d < DP || s.dv < DP)
+            for (int i = lane; i < kBytes / 16; i += 32) reinterpret_cast<uint4*>(memory)[i] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+    }
+    // Where the step at w comes from.
+    __device__ __forceinline__ void locate(const AttendArgs& a, const Walk& w) {
+        const View& s = a.s;
+        live = 0;
+        if (w.left <= 0) return;
+        const int first = w.k * KEYS, key = first + (whole ? 0 : (threadIdx.x & 31) % KEYS);
+        bool valid = false;
+        if (key < w.len) {
+            const int tp = page_of(s, key), slot = key - tp * s.page + (whole ? row0 : 0);
+            const int pg = checked_page(s, s.table, w.b, tp, a.status);
+            if (pg >= 0) {
+                k = a.kp + pg * s.k_page + w.h * s.k_head + slot * s.k_token + (whole ? ch * 16 : 0);
+                v = a.vp + pg * s.v_page + w.h * s.v_head + slot * s.v_token + (whole ? ch * 16 : 0);
+                valid = true;
             }
         }
-        if (lane == 0) {
-            row[dv] = st.m[g];
-            row[dv + 1] = l;
+        const uint32_t all = (uint32_t)((1ull << KEYS) - 1);
+        if (whole) live = !valid ? 0u : w.len - first >= KEYS ? all : (1u << (w.len - first)) - 1;
+        else live = __ballot_sync(0xffffffffu, valid) & all;
+    }
+    // Starts the copies of the located step; a value row that is not there is
+    // filled with zeros (its weight is 0, and 0 times what lay there may not be).
+    __device__ __forceinline__ void fetch(const AttendArgs& a, int stage) {
+        const View& s = a.s;
+        const uint32_t kd = mem + stage * kStage, vd = kd + KEYS * kRow;
+        const int ck = s.d * ESIZE / 16, cv = s.dv * ESIZE / 16;
+        if (whole && live == (uint32_t)((1ull << KEYS) - 1)) {
+            const char *ks = k, *vs = v;
+            const int64_t kstep = kPass * s.k_token, vstep = kPass * s.v_token;
+#pragma unroll
+            for (int i = 0; i < KEYS / kPass; ++i) {
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    if (ch + p * 32 < ck) cp_async16(kd + i * kPass * kRow + p * 512, ks + p * 512);
+                    if (ch + p * 32 < cv) cp_async16(vd + i * kPass * kRow + p * 512, vs + p * 512);
+                }
+                ks += kstep;
+                vs += vstep;
+            }
+            return;
+        }
+        for (int i = 0; i < KEYS / kPass; ++i) {
+            const int row = i * kPass + row0;
+            const char *ks, *vs;
+            if (whole) {
+                ks = k + i * kPass * s.k_token;
+                vs = v + i * kPass * s.v_token;
+            } else {
+                ks = shfl_ptr(k, row) + ch * 16;
+                vs = shfl_ptr(v, row) + ch * 16;
+            }
+            const bool there = (live >> row) & 1;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                if (there && ch + p * 32 < ck) cp_async16(kd + i * kPass * kRow + p * 512, ks + p * 512);
+                if (ch + p * 32 < cv) {
+                    const uint32_t to = vd + i * kPass * kRow + p * 512;
+                    if (there) cp_async16(to, vs + p * 512);
+                    else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+                }
+            }
         }
     }
-}
+};
 
 // No key was summed (every one masked, or none there).  A NaN among the logits
 // leaves l NaN and is no such row.
@@ -169,48 +216,40 @@ __device__ __forceinline__ float log_sum(float m, float l) {
     return nothing(m, l) ? m : (float)(((double)m + log2((double)l)) * 0.69314718055994530942);
 }
 
-// Joins the block's warps (shared, [warps][RG][dv + 2]) and writes the rows:
-// as partial rows (O, l, m) at `part`, or finished to out / lse.
-template <int RG>
-__device__ __forceinline__ void join_warps(const AttendArgs& a, const float* merge, float* part, int64_t row0,
-                                           int rows) {
+// Joins a coreset block's warps (shared, [warps][RG][dv + 2]) into partial rows.
+template <int RG, int WARPS>
+__device__ __forceinline__ void join_warps(const AttendArgs& a, const float* merge, int index, int rows) {
     const int dv = a.s.dv, ld = dv + 2;
     for (int g = 0; g < rows; ++g) {
         const float* r = merge + g * ld;
         float m = -CUDART_INF_F;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, r[w * RG * ld + dv]);
+        for (int w = 0; w < WARPS; ++w) m = fmaxf(m, r[w * RG * ld + dv]);
         const float ref = m == -CUDART_INF_F ? 0.f : m;
-        float f[kWarps], l = 0.f;
+        float f[WARPS], l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             f[w] = ex2(r[w * RG * ld + dv] - ref);
             l += f[w] * r[w * RG * ld + dv + 1];
         }
-        for (int c = threadIdx.x; c < dv; c += kThreads) {
+        const int64_t row = (int64_t)index * a.rows + g;
+        float* to = a.cparts + row * dv;
+        for (int c = threadIdx.x; c < dv; c += WARPS * 32) {
             float o = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) o = fmaf(f[w], r[w * RG * ld + c], o);
-            if (part) part[(int64_t)g * c1_row(dv) + c] = o;
-            else a.out[(row0 + g) * dv + c] = nothing(m, l) ? 0.f : o / l;
+            for (int w = 0; w < WARPS; ++w) o = fmaf(f[w], r[w * RG * ld + c], o);
+            to[c] = o;
         }
-        if (threadIdx.x == 0) {
-            if (part) {
-                part[(int64_t)g * c1_row(dv) + dv] = l;
-                part[(int64_t)g * c1_row(dv) + dv + 1] = m;
-            } else if (a.lse) {
-                a.lse[row0 + g] = log_sum(m, l);
-            }
-        }
+        if (threadIdx.x == 0) a.cparts_lm[row] = make_float2(l, m);
     }
 }
 
 // Query rows of one unit into shared memory as fp32, scaled to log2 units;
 // rows past the group are zero.
-template <typename T, int RG>
+template <typename T, int RG, int WARPS>
 __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int g0, int rows, float* q) {
     const T* src = static_cast<const T*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
-    for (int i = threadIdx.x; i < RG * a.s.d; i += kThreads) {
+    for (int i = threadIdx.x; i < RG * a.s.d; i += WARPS * 32) {
         const int g = i / a.s.d, c = i - g * a.s.d;
         q[i] = g < rows ? to_f32(src[g * a.q_head + c]) * a.qscale : 0.f;
     }
@@ -219,7 +258,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int g0,
 // Shared memory of one coreset block, in bytes: two stages a warp of NT keys
 // and their rows of W (as they lie in memory, dv + 1 values each).  The warps'
 // sums go where the stages were.
-template <int NT, int RG>
+template <int NT, int RG, int WARPS>
 struct CoresetSmem {
     int k_row, w_row, w, stage, q, p, total;
     __host__ __device__ CoresetSmem(int d, int dv, int esize) {
@@ -228,10 +267,10 @@ struct CoresetSmem {
         w_row = (dv + 1) * 4;
         w = NT * k_row;
         stage = (w + NT * w_row + 15) / 16 * 16;
-        const int stages = kWarps * 2 * stage, merge = kWarps * RG * (dv + 2) * 4;
+        const int stages = WARPS * 2 * stage, merge = WARPS * RG * (dv + 2) * 4;
         q = ((stages > merge ? stages : merge) + 15) / 16 * 16;
         p = q + RG * d * 4;
-        total = p + kWarps * NT * RG * 4;
+        total = p + WARPS * NT * RG * 4;
     }
 };
 
@@ -246,10 +285,10 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // summed; a lane holds columns lane, lane + 32, ... and the row's last value is
 // its weight in the normaliser.  Sums in fp32 on CUDA cores: W's values cancel
 // one another, and there are few rows.
-template <typename T, int RG, int NT, int COLS>
+template <typename T, int RG, int NT, int COLS, int WARPS>
 __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
     const View& s = a.s;
-    const CoresetSmem<NT, RG> L(s.d, s.dv, sizeof(T));
+    const CoresetSmem<NT, RG, WARPS> L(s.d, s.dv, sizeof(T));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* q = reinterpret_cast<float*>(smem + L.q);
     float* p = reinterpret_cast<float*>(smem + L.p) + warp * NT * RG;
@@ -272,7 +311,7 @@ __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
             const char* k = static_cast<const char*>(a.Ks) + (base + at) * s.d * (int64_t)sizeof(T);
             int row = lane / ck, c = lane - row * ck;
             for (int i = lane; i < NT * ck; i += 32) {
-                cp_async16(kd + row * L.k_row + c * 16, k + (row < live ? i : 0) * 16, row < live);
+                if (row < live) cp_async16(kd + row * L.k_row + c * 16, k + i * 16);
                 for (c += 32; c >= ck; c -= ck) ++row;
             }
             const float* w = a.W + (base + at) * (s.dv + 1);
@@ -282,7 +321,7 @@ __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
     };
     int at = first + warp * NT;
     load(0, at);
-    load_queries<T, RG>(a, b, h * s.group + rt * a.rows, rows, q);
+    load_queries<T, RG, WARPS>(a, b, h * s.group + rt * a.rows, rows, q);
     __syncthreads();
     float m[RG], l[RG], o[RG][COLS];
 #pragma unroll
@@ -292,8 +331,8 @@ __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
 #pragma unroll
         for (int i = 0; i < COLS; ++i) o[g][i] = 0.f;
     }
-    for (int stage = 0; at < last; at += kWarps * NT, stage ^= 1) {
-        load(stage ^ 1, at + kWarps * NT);
+    for (int stage = 0; at < last; at += WARPS * NT, stage ^= 1) {
+        load(stage ^ 1, at + WARPS * NT);
         cp_async_wait<1>();
         __syncwarp();
         const char* krows = stages + stage * L.stage;
@@ -352,153 +391,183 @@ __device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
         }
     }
     __syncthreads();
-    join_warps<RG>(a, merge, a.cparts + (int64_t)index * a.rows * c1_row(s.dv), 0, rows);
+    join_warps<RG, WARPS>(a, merge, index, rows);
 }
 
-// fp32 pages, on CUDA cores (their products keep 24 bits).  Each warp takes NT keys
-// of every 4 NT-key tile through its own two stages of shared memory (filled
-// by cp.async, so warps never wait for one another inside a unit); a lane
-// holds one key's logits for the RG query rows, then four value columns.
-template <int RG, int NT, int NVI>
-__global__ void __launch_bounds__(kThreads) cache_attend_simt_kernel(const AttendArgs a) {
-    using T = float;
+// fp32 pages, on CUDA cores (their products keep 24 bits): 8 keys a step, two
+// stages a warp.  For the logits a lane holds one key and a quarter of the
+// width, for the values four columns (and, where fewer than 32 lanes cover the
+// width, every second key).  DP: d and dv rounded up to 64, 128 or 256.
+constexpr int kSimtKeys = 8;
+constexpr int kSimtStages = 2;
+
+template <int DP> using SimtRing = Ring<kSimtKeys, DP, 4, kSimtStages>;
+template <int DP, int RG>
+struct SimtSmem {
+    static constexpr int q = SimtRing<DP>::kBytes, p = q + RG * DP * 4, warp = p + kSimtKeys * RG * 4;
+    static constexpr int total = kSimtWarps * warp;
+};
+
+template <int DP, int RG>
+__global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(const AttendArgs a) {
+    constexpr int KEYS = kSimtKeys, kChunks = DP / 4;
+    constexpr int kGroups = kChunks < 32 ? 32 / kChunks : 1;      // key groups of the value sums
+    constexpr int kCols = kChunks < 32 ? 1 : kChunks / 32;        // a lane's column quadruples
+    using L = SimtSmem<DP, RG>;
     extern __shared__ __align__(128) char smem[];
-    __shared__ int64_t place_sh[4 + kWarps];
+    __shared__ int place_sh[2 + kSimtWarps];
     grid_dependents_launch();
     const View& s = a.s;
-    const int blocks = a.blocks;
-    if ((int)blockIdx.x >= blocks) {
-        coreset_block<T, RG, NT, NVI * 4>(a, blockIdx.x - blocks, smem);
+    if ((int)blockIdx.x >= a.blocks) {
+        coreset_block<float, RG, 8, DP / 32, kSimtWarps>(a, blockIdx.x - a.blocks, smem);
         return;
     }
-    constexpr int kTile = kWarps * NT;
-    const SimtSmem<NT, RG> L(s.d, s.dv, sizeof(T));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* q = reinterpret_cast<float*>(smem + L.q);
-    float* p = reinterpret_cast<float*>(smem + L.p) + warp * NT * RG;
-    float* merge = reinterpret_cast<float*>(smem + L.merge);
-    char* stages = smem + warp * L.warp;
-    const int per_tile = s.hkv * a.row_tiles;
-    const int c = blockIdx.x;
-    const Place at = find_place<kThreads>(s, a.lens, kTile, per_tile, c, blocks, -1, a.status, place_sh);
-    if (c >= at.blocks) return;
-    int64_t t = block_first(at.total, c, at.blocks);
-    const int64_t t_last = block_first(at.total, c + 1, at.blocks);
-    int b = at.b;
-    int len = checked_len(a.lens, b, s.cap, a.status);
-    int tiles = (len + kTile - 1) / kTile;
-    int in_b = (int)((t - at.before) / tiles);          // unit within the sequence: h * row_tiles + rt
-    int k0 = (int)((t - at.before) % tiles);
-    const int ck = s.d * (int)sizeof(T) / 16, cv = s.dv * (int)sizeof(T) / 16;
-    const int vchunks = s.dv / 4;
-    const int groups = vchunks <= 8 ? 4 : vchunks <= 16 ? 2 : 1;   // key groups when few columns fill a warp
-    const int cols = 32 / groups;
-    while (t < t_last) {
-        const int k1 = (int)min((int64_t)tiles, k0 + (t_last - t));
-        const int h = in_b / a.row_tiles, rt = in_b % a.row_tiles;
-        const int rows = min(a.rows, s.group - rt * a.rows), g0 = h * s.group + rt * a.rows;
-        load_queries<T, RG>(a, b, g0, rows, q);
-        __syncthreads();
-        Running<RG, NVI> st;
-        st.clear();
-        const char* kh = a.kp + h * s.k_head;
-        const char* vh = a.vp + h * s.v_head;
-        // lane j < NT: where key j of tile i is
-        auto locate = [&](int i) {
-            KeyPlace w{0, 0, false};
-            const int key = i * kTile + warp * NT + lane;
-            if (lane < NT && i < k1 && key < len) {
-                const int tp = key / s.page, slot = key - tp * s.page;
-                const int pg = checked_page(s, s.table, b, tp, a.status);
-                if (pg >= 0) {
-                    w.k = pg * s.k_page + slot * s.k_token;
-                    w.v = pg * s.v_page + slot * s.v_token;
-                    w.valid = true;
-                }
-            }
-            return w;
-        };
-        auto load = [&](int stage, const KeyPlace& w) {
-            const uint32_t kd = (uint32_t)__cvta_generic_to_shared(stages + stage * L.stage);
-            const uint32_t vd = kd + NT * L.k_row;
-            for (int i = lane, n = (NT * ck + 31) / 32; n > 0; --n, i += 32) {
-                const int row = i / ck, ch = i - row * ck;
-                const int64_t off = __shfl_sync(0xffffffffu, w.k, row & (NT - 1));
-                const bool ok = __shfl_sync(0xffffffffu, (int)w.valid, row & (NT - 1)) != 0;
-                if (row < NT) cp_async16(kd + row * L.k_row + ch * 16, kh + off + ch * 16, ok);
-            }
-            for (int i = lane, n = (NT * cv + 31) / 32; n > 0; --n, i += 32) {
-                const int row = i / cv, ch = i - row * cv;
-                const int64_t off = __shfl_sync(0xffffffffu, w.v, row & (NT - 1));
-                const bool ok = __shfl_sync(0xffffffffu, (int)w.valid, row & (NT - 1)) != 0;
-                if (row < NT) cp_async16(vd + row * L.v_row + ch * 16, vh + off + ch * 16, ok);
-            }
-        };
-        KeyPlace next = locate(k0);
-        uint32_t mask = __ballot_sync(0xffffffffu, next.valid);
-        load(0, next);
+    char* mem = smem + warp * L::warp;
+    float* q = reinterpret_cast<float*>(mem + L::q);
+    float* p = reinterpret_cast<float*>(mem + L::p);
+    const int c = blockIdx.x * kSimtWarps + warp;
+    const Place at = find_place<kSimtWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, a.workers,
+                                                 blockIdx.x * kSimtWarps, -1, a.status, place_sh);
+    Walk now, ahead;
+    now.start(a, at, c, KEYS);
+    if (now.left <= 0) return;
+    ahead = now;
+    SimtRing<DP> ring;
+    ring.init(a, mem);
+    uint32_t masks = 0;   // the live keys of the steps in the ring, a byte each, the next one lowest after a fetch
+    auto fetch = [&](int stage) {   // the next step's copies; where the one after it is
+        masks = masks >> 8 | ring.live << 8;
+        if (ahead.left > 0) {
+            ring.fetch(a, stage);
+            ahead.next(a, KEYS);
+            ring.locate(a, ahead);   // (a step early: the table entry is there when it is used)
+        }
         cp_async_commit();
-        for (int i = k0; i < k1; ++i) {
-            const int stage = (i - k0) & 1;
-            const uint32_t live = mask;
-            next = locate(i + 1);
-            mask = __ballot_sync(0xffffffffu, next.valid);
-            if (i + 1 < k1) load(stage ^ 1, next);
-            cp_async_commit();
-            cp_async_wait<1>();
-            __syncwarp();
-            const char* krows = stages + stage * L.stage;
-            const char* vrows = krows + NT * L.k_row;
-            float x[RG];
-            tile_logits<T, RG, NT>(krows, L.k_row, q, s.d, x);
-            const int key = lane % NT;
-            const bool ok = (live >> key) & 1;
+    };
+    ring.locate(a, ahead);
+    fetch(0);
+    const int key = lane % KEYS, part = lane / KEYS;
+    int stage = 0;
+    while (now.left > 0) {
+        // the share of one unit: steps now.k up to `last`
+        const int rows = min(a.rows, s.group - now.rt * a.rows), g0 = now.h * s.group + now.rt * a.rows;
+        const int start = now.k, last = min(now.tiles, now.k + now.left);
+        const int64_t row0 = (int64_t)now.b * s.hq + g0;
+        const float* src = static_cast<const float*>(a.Q) + now.b * a.q_batch + (int64_t)g0 * a.q_head;
+#pragma unroll 4
+        for (int i = lane; i < RG * DP; i += 32) {
+            const int g = i / DP, col = i % DP;
+            q[i] = g < rows && col < s.d ? src[g * a.q_head + col] * a.qscale : 0.f;
+        }
+        float m[RG], l[RG], o[RG][kCols * 4];
 #pragma unroll
-            for (int g = 0; g < RG; ++g) x[g] = ok ? x[g] : -CUDART_INF_F;
-            if (a.logits && lane < NT) {
-                const int pos = i * kTile + warp * NT + key;
-                if (pos < len)
-                    for (int g = 0; g < rows; ++g)
-                        a.logits[((int64_t)b * s.hq + g0 + g) * s.cap + pos] = x[g];
+        for (int g = 0; g < RG; ++g) {
+            m[g] = -CUDART_INF_F;
+            l[g] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kCols * 4; ++i) o[g][i] = 0.f;
+        }
+        for (int step = start; step < last; ++step) {
+        fetch(stage ^ 1);
+        const uint32_t mask = masks & 0xff;
+        cp_async_wait<1>();
+        __syncwarp();
+        const char* krows = mem + stage * SimtRing<DP>::kStage;
+        const char* vrows = krows + KEYS * SimtRing<DP>::kRow;
+        float x[RG];
+#pragma unroll
+        for (int g = 0; g < RG; ++g) x[g] = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < kChunks / 4; ++i) {
+            const int ch = part + 4 * i;
+            const float4 k4 = *reinterpret_cast<const float4*>(krows + key * SimtRing<DP>::kRow + ch * 16);
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                const float4 q4 = *reinterpret_cast<const float4*>(q + g * DP + ch * 4);
+                x[g] = fmaf(k4.x, q4.x, x[g]);
+                x[g] = fmaf(k4.y, q4.y, x[g]);
+                x[g] = fmaf(k4.z, q4.z, x[g]);
+                x[g] = fmaf(k4.w, q4.w, x[g]);
             }
-            tile_weights<RG, NT, NVI>(st, x, p);
-            __syncwarp();
-            for (int j = lane / cols; j < NT; j += groups) {
-                float w[RG];
+        }
+        const bool ok = (mask >> key) & 1;
+        const int pos = step * KEYS + key;
 #pragma unroll
-                for (int g = 0; g < RG; ++g) w[g] = p[j * RG + g];
+        for (int g = 0; g < RG; ++g) {
+            x[g] += __shfl_xor_sync(0xffffffffu, x[g], 8);
+            x[g] += __shfl_xor_sync(0xffffffffu, x[g], 16);
+            if (!ok) x[g] = -CUDART_INF_F;
+            if (a.logits && part == 0 && pos < now.len && g < rows)
+                a.logits[(row0 + g) * s.cap + pos] = x[g];
+            float top = x[g];
 #pragma unroll
-                for (int n = 0; n < NVI; ++n) {
-                    const int ch = lane % cols + n * cols;
-                    if (ch < vchunks) {
-                        float y[4];
-                        load_chunk<float>(vrows + j * L.v_row + ch * 16, y);
+            for (int e = 1; e < KEYS; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+            if (top > m[g] + 8.f) {   // (the reference follows the maximum when it has grown by 2^8, see below)
+                const float f = ex2(m[g] - top);   // 0 where nothing was summed yet
+                m[g] = top;
+                l[g] *= f;
 #pragma unroll
-                        for (int g = 0; g < RG; ++g)
+                for (int i = 0; i < kCols * 4; ++i) o[g][i] *= f;
+            }
+            // nothing but masked keys so far: the reference is 0, every weight 2^-inf = 0
+            const float w = ex2(x[g] - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
+            if (part == 0) {
+                l[g] += w;
+                p[key * RG + g] = w;
+            }
+        }
+        __syncwarp();
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) st.o[g][n * 4 + e] = fmaf(w[g], y[e], st.o[g][n * 4 + e]);
-                    }
+        for (int j0 = 0; j0 < KEYS; j0 += kGroups) {
+            const int j = j0 + (kGroups > 1 ? lane / kChunks : 0);
+            float w[RG];
+#pragma unroll
+            for (int g = 0; g < RG; ++g) w[g] = p[j * RG + g];
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) {
+                const int ch = (kGroups > 1 ? lane % kChunks : lane) + n * 32;
+                const float4 y = *reinterpret_cast<const float4*>(vrows + j * SimtRing<DP>::kRow + ch * 16);
+#pragma unroll
+                for (int g = 0; g < RG; ++g) {
+                    o[g][n * 4] = fmaf(w[g], y.x, o[g][n * 4]);
+                    o[g][n * 4 + 1] = fmaf(w[g], y.y, o[g][n * 4 + 1]);
+                    o[g][n * 4 + 2] = fmaf(w[g], y.z, o[g][n * 4 + 2]);
+                    o[g][n * 4 + 3] = fmaf(w[g], y.w, o[g][n * 4 + 3]);
                 }
             }
-            __syncwarp();
         }
-        cp_async_wait<0>();
-        leave_state<RG, NVI>(st, merge + warp * RG * (s.dv + 2), s.dv, groups);
-        __syncthreads();
-        const bool whole = k0 == 0 && k1 == tiles && !a.csplits && !a.logits;
-        const int64_t unit = (int64_t)b * per_tile + in_b;
-        join_warps<RG>(a, merge, whole ? nullptr : a.parts + (unit + c) * a.rows * c1_row(s.dv),
-                       (int64_t)b * s.hq + g0, rows);
-        __syncthreads();
-        t += k1 - k0;
-        k0 = 0;
-        if (t < t_last && ++in_b == per_tile) {
-            in_b = 0;
-            do {
-                len = checked_len(a.lens, ++b, s.cap, a.status);
-            } while (len == 0);
-            tiles = (len + kTile - 1) / kTile;
+        __syncwarp();
+        stage ^= 1;
         }
+        // finished rows where the share is the whole unit, else partial rows
+        const bool whole = start == 0 && last == now.tiles && !a.csplits && !a.logits;
+        const int64_t part_row = ((int64_t)(now.b * s.hkv + now.h) * a.row_tiles + now.rt + c) * a.rows;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+#pragma unroll
+            for (int e = 1; e < 32; e <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], e);
+#pragma unroll
+            for (int e = 32 / kGroups; e < 32; e <<= 1)
+#pragma unroll
+                for (int i = 0; i < kCols * 4; ++i) o[g][i] += __shfl_xor_sync(0xffffffffu, o[g][i], e);
+            if (g >= rows) continue;
+            const bool none = nothing(m[g], l[g]);
+            float* to = whole ? a.out + (row0 + g) * s.dv : a.parts + (part_row + g) * s.dv;
+#pragma unroll
+            for (int n = 0; n < kCols; ++n) {
+                const int col = (lane + n * 32) * 4;
+                if (lane < 32 / kGroups && col < s.dv)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        to[col + e] = whole ? (none ? 0.f : o[g][n * 4 + e] / l[g]) : o[g][n * 4 + e];
+            }
+            if (lane == 0) {
+                if (!whole) a.parts_lm[part_row + g] = make_float2(l[g], m[g]);
+                else if (a.lse) a.lse[row0 + g] = log_sum(m[g], l[g]);
+            }
+        }
+        now.skip(a, last - start, KEYS);
     }
 }
 
@@ -519,7 +588,7 @@ __device__ __forceinline__ void ldmatrix4t(uint32_t r[4], uint32_t addr) {
 // a b, 16 x 8 x 16, bf16 in, fp32 sums.
 __device__ __forceinline__ void mma16816_new(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%10,%10,%10,%10};"
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -527,7 +596,7 @@ __device__ __forceinline__ void mma16816_new(float c[4], uint32_t a0, uint32_t a
 // c += a b.
 __device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                  "{%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -550,139 +619,97 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t t[3]) {
     }
 }
 
-// (x, y) += (u, v) as one packed fp32 addition.
-__device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tadd.rn.f32x2 a, a, b;\n\t"
-        "mov.b64 {%0, %1}, a;\n\t}"
-        : "+f"(x), "+f"(y)
-        : "f"(u), "f"(v));
+// Pairs of fp32 values in one 64-bit register, added and multiplied as one.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 both(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t p;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
+    return p;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
+    return p;
 }
 
 constexpr int kMmaKeys = 16;     // keys of one warp's step
-constexpr int kMmaStages = 3;
+// Stages of a warp's ring, and warps of a block: what fits two blocks an SM (one for the widest rows).
+template <int DP> constexpr int kMmaStages = DP > 128 ? 2 : 3;
+template <int DP> constexpr int kMmaWarps = DP > 128 ? 6 : 4;
 template <int DP> constexpr int kCoresetKeys = DP > 128 ? 8 : 16;   // (two stages of wider rows leave too little room)
+
+template <int DP> using MmaRing = Ring<kMmaKeys, DP, 2, kMmaStages<DP>>;
 
 // bf16 pages on tensor cores (mma.sync: a group's 1 to 16 query rows fill one
 // 16-row tile at most, and the pass is bound by the bytes of the keys and
 // values, so the wider tcgen05 tiles would only hold more padding).  A warp
-// takes 16 keys of every 64-key tile through its own ring of three stages;
-// 128-byte groups of a row are XOR-swizzled by the row so that ldmatrix reads
-// without bank conflicts.  DP: d and dv rounded up to 64, 128 or 256 (columns
-// past the width are zeros).
+// takes 16 keys a step.  DP: d and dv rounded up to 64, 128 or 256.
 // SETS: how the weights' three terms meet the 16 rows of the value product.
 //   1  up to 4 query rows, each four times in the tile (r, r + 4, r + 8, r + 12):
 //      the copies carry the terms, so one product adds all three
 //   2  up to 8 rows, each twice: two products
 //   3  up to 16 rows: three products
 template <int DP, int SETS>
-__global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(const AttendArgs a) {
     using bf16 = __nv_bfloat16;
     constexpr int kRows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
-    constexpr int kChunks = DP / 8;                        // 16-byte pieces of a row
-    constexpr int kRowBytes = DP * 2;
-    constexpr int kStage = 2 * kMmaKeys * kRowBytes;       // keys, then values
-    constexpr int kTile = kWarps * kMmaKeys;
-    constexpr int kPerLoad = 32 / kChunks > 0 ? 32 / kChunks : 1;   // rows of one warp-wide load
-    constexpr int kLoads = kMmaKeys * kChunks / 32;
+    constexpr int KEYS = kMmaKeys, kRow = MmaRing<DP>::kRow;
+    constexpr int kStages = kMmaStages<DP>, kBlockWarps = kMmaWarps<DP>;
+    constexpr int kMine = SETS == 3 ? 2 : 1;               // rows of a lane
     extern __shared__ __align__(128) char smem[];
-    __shared__ int64_t place_sh[4 + kWarps];
+    __shared__ int place_sh[2 + kBlockWarps];
     grid_dependents_launch();
     const View& s = a.s;
-    const int blocks = a.blocks;
-    if ((int)blockIdx.x >= blocks) {
-        coreset_block<bf16, kRows, kCoresetKeys<DP>, DP / 32>(a, blockIdx.x - blocks, smem);
+    if ((int)blockIdx.x >= a.blocks) {
+        coreset_block<bf16, kRows, kCoresetKeys<DP>, DP / 32, kBlockWarps>(a, blockIdx.x - a.blocks, smem);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane >> 2, pair = lane & 3;           // fragment row and column pair
-    char* stages = smem + warp * kMmaStages * kStage;
-    const uint32_t stages_u = (uint32_t)__cvta_generic_to_shared(stages);
-    const int per_tile = s.hkv * a.row_tiles;
-    const int c = blockIdx.x;
-    const Place at = find_place<kThreads>(s, a.lens, kTile, per_tile, c, blocks, -1, a.status, place_sh);
-    if (c >= at.blocks) return;
-    int64_t t = block_first(at.total, c, at.blocks);
-    const int64_t t_last = block_first(at.total, c + 1, at.blocks);
-    int b = at.b;
-    int len = checked_len(a.lens, b, s.cap, a.status);
-    int tiles = (len + kTile - 1) / kTile;
-    int in_b = (int)((t - at.before) / tiles);
-    int k0 = (int)((t - at.before) % tiles);
-    const int ck = s.d / 8, cv = s.dv / 8;
-    const bool whole_pages = s.page % kMmaKeys == 0;       // 16 keys of a step then share a page
-    while (t < t_last) {
-        const int k1 = (int)min((int64_t)tiles, k0 + (t_last - t));
-        const int h = in_b / a.row_tiles, rt = in_b % a.row_tiles;
-        const int rows = min(a.rows, s.group - rt * a.rows), g0 = h * s.group + rt * a.rows;
-        const char* kh = a.kp + h * s.k_head;
-        const char* vh = a.vp + h * s.v_head;
-        float o[DP / 8][4];
-#pragma unroll
-        for (int n = 0; n < DP / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-        constexpr int kMine = SETS == 3 ? 2 : 1;           // rows of this lane
-        float m[kMine], l[kMine];
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
-
-        // lane j < 16: where key j of tile i is, and how many keys there are
-        auto locate = [&](int i) {
-            KeyPlace w{0, 0, false};
-            const int key = i * kTile + warp * kMmaKeys + (whole_pages ? 0 : lane & 15);
-            if (i < k1 && key < len) {
-                const int tp = key / s.page, slot = key - tp * s.page;
-                const int pg = checked_page(s, s.table, b, tp, a.status);
-                if (pg >= 0) {
-                    w.k = pg * s.k_page + slot * s.k_token;
-                    w.v = pg * s.v_page + slot * s.v_token;
-                    w.valid = true;
-                }
-            }
-            return w;
-        };
-        auto live_keys = [&](int i, const KeyPlace& w) {
-            const int n = len - (i * kTile + warp * kMmaKeys);
-            if (i >= k1 || n <= 0) return 0u;
-            if (!whole_pages) return __ballot_sync(0xffffffffu, w.valid) & 0xffffu;
-            return w.valid ? (n >= kMmaKeys ? 0xffffu : (1u << n) - 1) : 0u;
-        };
-        auto load = [&](int stage, const KeyPlace& w, uint32_t live) {
-            const uint32_t kd = stages_u + stage * kStage, vd = kd + kMmaKeys * kRowBytes;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int row = kChunks >= 32 ? i * 32 / kChunks : i * kPerLoad + lane / kChunks;
-                const int ch = lane % kChunks;
-                int64_t ko = w.k, vo = w.v;
-                if (whole_pages) {
-                    ko += row * s.k_token;
-                    vo += row * s.v_token;
-                } else {
-                    ko = __shfl_sync(0xffffffffu, w.k, row);
-                    vo = __shfl_sync(0xffffffffu, w.v, row);
-                }
-                const bool ok = (live >> row) & 1;
-                const uint32_t to = row * kRowBytes + (ch ^ (row & 7)) * 16;
-                const bool kok = ok && ch < ck, vok = ok && ch < cv;
-                cp_async16(kd + to, kok ? kh + ko + ch * 16 : a.kp, kok);
-                cp_async16(vd + to, vok ? vh + vo + ch * 16 : a.vp, vok);
-            }
-        };
-        uint32_t live[kMmaStages];
-        KeyPlace next;
-#pragma unroll
-        for (int p = 0; p < kMmaStages - 1; ++p) {
-            next = locate(k0 + p);
-            live[p] = live_keys(k0 + p, next);
-            if (k0 + p < k1) load(p, next, live[p]);
-            cp_async_commit();
+    const int c = blockIdx.x * kBlockWarps + warp;
+    const Place at = find_place<kBlockWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, a.workers,
+                                                  blockIdx.x * kBlockWarps, -1, a.status, place_sh);
+    Walk now, ahead;
+    now.start(a, at, c, KEYS);
+    if (now.left <= 0) return;
+    ahead = now;
+    MmaRing<DP> ring;
+    char* mem = smem + warp * MmaRing<DP>::kBytes;
+    const uint32_t stages = (uint32_t)__cvta_generic_to_shared(mem);
+    ring.init(a, mem);
+    uint64_t masks = 0;   // the live keys of the steps in the ring, 16 bits each, the next one lowest after a fetch
+    auto fetch = [&](int stage) {   // the next step's copies; where the one after it is
+        masks = masks >> 16 | (uint64_t)ring.live << (16 * (kStages - 1));
+        if (ahead.left > 0) {
+            ring.fetch(a, stage);
+            ahead.next(a, KEYS);
+            ring.locate(a, ahead);   // (a step early: the table entry is there when it is used)
         }
-        next = locate(k0 + kMmaStages - 1);
+        cp_async_commit();
+    };
+    ring.locate(a, ahead);
+#pragma unroll 1
+    for (int p = 0; p < kStages - 1; ++p) fetch(p);
+    int stage = 0;
+    while (now.left > 0) {
+        // the share of one unit: steps now.k up to `last`
+        const int rows = min(a.rows, s.group - now.rt * a.rows), g0 = now.h * s.group + now.rt * a.rows;
+        const int start = now.k, last = min(now.tiles, now.k + now.left);
+        const int64_t row0 = (int64_t)now.b * s.hq + g0;
         // Query fragments, as they are (the logits are scaled in fp32): rows
         // quad and, where the rows are not copies, quad + 8.
         uint32_t q[DP / 16][SETS == 3 ? 4 : 2];
         {
-            const bf16* src = static_cast<const bf16*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
+            const bf16* src = static_cast<const bf16*>(a.Q) + now.b * a.q_batch + (int64_t)g0 * a.q_head;
             auto two = [&](int row, int col) {
                 uint32_t v = 0;
                 if (row < rows && col < s.d) {
@@ -705,197 +732,179 @@ __global__ void __launch_bounds__(kThreads) cache_attend_mma_kernel(const Attend
                 }
             }
         }
-        int stage = 0;
-        for (int i = k0; i < k1; ++i) {
-            cp_async_wait<kMmaStages - 2>();
-            __syncwarp();
-            const uint32_t kd = stages_u + stage * kStage, vd = kd + kMmaKeys * kRowBytes;
-            const uint32_t mask = live[0];
-            {   // the stage read in the last step is free: load three tiles ahead
-                const int ahead = i + kMmaStages - 1, to = stage == 0 ? kMmaStages - 1 : stage - 1;
-                const uint32_t lv = live_keys(ahead, next);
-                if (ahead < k1) load(to, next, lv);
-                cp_async_commit();
-                next = locate(ahead + 1);
+        uint64_t o[DP / 8][2];                             // pairs of fp32 sums: row quad, row quad + 8
+        float m[kMine], l[kMine];
 #pragma unroll
-                for (int p = 0; p < kMmaStages - 2; ++p) live[p] = live[p + 1];
-                live[kMmaStages - 2] = lv;
+        for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
+        for (int step = start; step < last; ++step) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();
+        const uint32_t kd = stages + stage * MmaRing<DP>::kStage, vd = kd + KEYS * kRow;
+        fetch(stage == 0 ? kStages - 1 : stage - 1);       // the stage that the last step read is free
+        const uint32_t mask = (uint32_t)masks & 0xffffu;
+        // logits: keys 0..7 in x[0], 8..15 in x[1]
+        float x[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+        {
+            const int row = (lane & 7) + ((lane >> 4) << 3);
+            const uint32_t base = kd + row * kRow + ((lane >> 3) & 1) * 16;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                uint32_t f[4];
+                ldmatrix4(f, base + k * 32);
+                if (SETS == 3) {
+                    mma16816(x[0], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[0], f[1]);
+                    mma16816(x[1], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[2], f[3]);
+                } else {
+                    mma16816(x[0], q[k][0], q[k][0], q[k][1], q[k][1], f[0], f[1]);
+                    mma16816(x[1], q[k][0], q[k][0], q[k][1], q[k][1], f[2], f[3]);
+                }
             }
-            // logits: keys 0..7 in x[0], 8..15 in x[1]
-            float x[2][4];
+        }
+        uint32_t w[kMine][2][3];                           // weights' terms: [row][key octet][term]
+#pragma unroll
+        for (int r = 0; r < kMine; ++r) {
+            float y[4];
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-            {
-                const int row = (lane & 7) + ((lane >> 4) << 3);
-                const uint32_t base = kd + row * kRowBytes;
+                for (int e = 0; e < 2; ++e)
+                    y[2 * n + e] = x[n][2 * r + e] * a.qscale;
+            if (mask != 0xffffu)
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    uint32_t f[4];
-                    ldmatrix4(f, base + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
-                    if (SETS == 3) {
-                        mma16816(x[0], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[0], f[1]);
-                        mma16816(x[1], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[2], f[3]);
-                    } else {
-                        mma16816(x[0], q[k][0], q[k][0], q[k][1], q[k][1], f[0], f[1]);
-                        mma16816(x[1], q[k][0], q[k][0], q[k][1], q[k][1], f[2], f[3]);
-                    }
-                }
-            }
-            uint32_t w[kMine][2][3];                       // weights' terms: [row][key octet][term]
-#pragma unroll
-            for (int r = 0; r < kMine; ++r) {
-                float y[4];
+                for (int e = 0; e < 4; ++e)
+                    if (!((mask >> (e / 2 * 8 + pair * 2 + e % 2)) & 1)) y[e] = -CUDART_INF_F;
+            if (a.logits && quad + 8 * r < rows) {
+                const int pos = step * KEYS;
+                float* to = a.logits + (row0 + quad + 8 * r) * s.cap + pos;
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = n * 8 + pair * 2 + e;
+                        if (pos + key < now.len) to[key] = y[2 * n + e];
+                    }
+            }
+            float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // The reference follows the maximum only when it has grown by more than 2^8, which
+            // spares most steps the rescaling; weights up to 2^8 lose nothing in fp32.
+            const bool grow = top > m[r] + 8.f;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? ex2(m[r] - top) : 1.f;
+                if (grow) m[r] = top;
+                l[r] *= f;
+                const uint64_t ff = pair_of(f, f);
+#pragma unroll
+                for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        y[2 * n + e] = (mask >> (n * 8 + pair * 2 + e)) & 1 ? x[n][2 * r + e] * a.qscale
-                                                                            : -CUDART_INF_F;
-                if (a.logits) {
-                    const int g = quad + 8 * r;
-                    if (g < rows) {
-                        const int pos = i * kTile + warp * kMmaKeys;
-                        float* to = a.logits + ((int64_t)b * s.hq + g0 + g) * s.cap + pos;
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = n * 8 + pair * 2 + e;
-                                if (pos + key < len) to[key] = y[2 * n + e];
-                            }
-                    }
-                }
-                float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // The reference follows the maximum only when it has grown by more than 2^8, which
-                // spares most steps the rescaling; weights up to 2^8 lose nothing in fp32.
-                const bool grow = top > m[r] + 8.f;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? ex2(m[r] - top) : 1.f;
-                    if (grow) m[r] = top;
-                    l[r] *= f;
-                    if (SETS == 3) {
-#pragma unroll
-                        for (int n = 0; n < DP / 8; ++n) o[n][2 * r] *= f, o[n][2 * r + 1] *= f;
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < DP / 8; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[n][e] *= f;
-                    }
-                }
-                const float ref = m[r] == -CUDART_INF_F ? 0.f : m[r];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = ex2(y[e] - ref);
-                l[r] += (y[0] + y[1]) + (y[2] + y[3]);
-                split_bf16(y[0], y[1], w[r][0]);
-                split_bf16(y[2], y[3], w[r][1]);
+                        if (SETS != 3 || e == r) o[n][e] = mul2(o[n][e], ff);
             }
-            // values
-            {
-                const int row = lane & 15;
-                const uint32_t base = vd + row * kRowBytes;
-                uint32_t p0 = 0, p1 = 0, p2 = 0, p3 = 0;
-                if (SETS == 1) {   // rows 0-3: term 0, 8-11: term 1, 4-7: term 2, 12-15: nothing
-                    const bool up = quad < 4;
-                    p0 = up ? w[0][0][0] : w[0][0][2]; p1 = up ? w[0][0][1] : 0u;
-                    p2 = up ? w[0][1][0] : w[0][1][2]; p3 = up ? w[0][1][1] : 0u;
-                }
+            const float ref = m[r] == -CUDART_INF_F ? 0.f : m[r];   // only masked keys so far: weights 2^-inf = 0
 #pragma unroll
-                for (int n = 0; n < DP / 16; ++n) {
-                    uint32_t f[4];
-                    ldmatrix4t(f, base + (((2 * n + (lane >> 4)) ^ (row & 7)) << 4));
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        // The product of the 16 keys by itself, then an ordinary fp32 addition: the
-                        // tensor cores' own accumulation does not round to nearest, and over the
-                        // thousands of steps of a long cache its errors all point one way
-                        // (4.3e-6 of the output at 131072 keys, 0.9e-6 so).
-                        float z[4];
-                        const uint32_t b0 = f[2 * u], b1 = f[2 * u + 1];
-                        if (SETS == 1) {
-                            mma16816_new(z, p0, p1, p2, p3, b0, b1);
-                        } else if (SETS == 2) {
-                            mma16816_new(z, w[0][0][0], w[0][0][1], w[0][1][0], w[0][1][1], b0, b1);
-                            mma16816(z, w[0][0][2], 0u, w[0][1][2], 0u, b0, b1);
-                        } else {
-                            mma16816_new(z, w[0][0][0], w[kMine - 1][0][0], w[0][1][0], w[kMine - 1][1][0], b0, b1);
-                            mma16816(z, w[0][0][1], w[kMine - 1][0][1], w[0][1][1], w[kMine - 1][1][1], b0, b1);
-                            mma16816(z, w[0][0][2], w[kMine - 1][0][2], w[0][1][2], w[kMine - 1][1][2], b0, b1);
-                        }
-                        add2(o[2 * n + u][0], o[2 * n + u][1], z[0], z[1]);
-                        add2(o[2 * n + u][2], o[2 * n + u][3], z[2], z[3]);
-                    }
-                }
-            }
-            stage = stage + 1 == kMmaStages ? 0 : stage + 1;
-            __syncwarp();
+            for (int e = 0; e < 4; ++e) y[e] = ex2(y[e] - ref);
+            l[r] += (y[0] + y[1]) + (y[2] + y[3]);
+            split_bf16(y[0], y[1], w[r][0]);
+            split_bf16(y[2], y[3], w[r][1]);
         }
-        cp_async_wait<0>();
-        __syncthreads();
-        // the warps' sums into the stages, which are idle now: [warp][kRows][dv + 2]
-        float* merge = reinterpret_cast<float*>(smem);
-        const int ld = s.dv + 2;
+        // values
+        {
+            const int row = lane & 15;
+            const uint32_t base = vd + row * kRow + (lane >> 4) * 16;
+            uint32_t p0 = 0, p1 = 0, p2 = 0, p3 = 0;
+            if (SETS == 1) {   // rows 0-3: term 0, 8-11: term 1, 4-7: term 2, 12-15: nothing
+                const bool up = quad < 4;
+                p0 = up ? w[0][0][0] : w[0][0][2]; p1 = up ? w[0][0][1] : 0u;
+                p2 = up ? w[0][1][0] : w[0][1][2]; p3 = up ? w[0][1][1] : 0u;
+            }
+#pragma unroll
+            for (int n = 0; n < DP / 16; ++n) {
+                uint32_t f[4];
+                ldmatrix4t(f, base + n * 32);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    // The product of the 16 keys by itself, then an ordinary fp32 addition: the
+                    // tensor cores' own accumulation does not round to nearest, and over the
+                    // thousands of steps of a long cache its errors all point one way
+                    // (4.3e-6 of the output at 131072 keys, 0.7e-6 so).
+                    float z[4];
+                    const uint32_t b0 = f[2 * u], b1 = f[2 * u + 1];
+                    if (SETS == 1) {
+                        mma16816_new(z, p0, p1, p2, p3, b0, b1);
+                    } else if (SETS == 2) {
+                        mma16816_new(z, w[0][0][0], w[0][0][1], w[0][1][0], w[0][1][1], b0, b1);
+                        mma16816(z, w[0][0][2], 0u, w[0][1][2], 0u, b0, b1);
+                    } else {
+                        mma16816_new(z, w[0][0][0], w[kMine - 1][0][0], w[0][1][0], w[kMine - 1][1][0], b0, b1);
+                        mma16816(z, w[0][0][1], w[kMine - 1][0][1], w[0][1][1], w[kMine - 1][1][1], b0, b1);
+                        mma16816(z, w[0][0][2], w[kMine - 1][0][2], w[0][1][2], w[kMine - 1][1][2], b0, b1);
+                    }
+                    o[2 * n + u][0] = add2(o[2 * n + u][0], pair_of(z[0], z[1]));
+                    o[2 * n + u][1] = add2(o[2 * n + u][1], pair_of(z[2], z[3]));
+                }
+            }
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        __syncwarp();
+        }
+        // finished rows where the share is the whole unit, else partial rows
+        const bool whole = start == 0 && last == now.tiles && !a.csplits && !a.logits;
+        const int64_t part_row = ((int64_t)(now.b * s.hkv + now.h) * a.row_tiles + now.rt + c) * a.rows;
 #pragma unroll
         for (int r = 0; r < kMine; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            const int g = quad + 8 * r;
-            float* row = merge + (warp * kRows + (g < kRows ? g : 0)) * ld;
+            // where rows 4 to 7 are copies, their lanes write every other pair of columns
+            const int g = SETS == 1 ? quad & 3 : quad + 8 * r;
+            const bool mine = g < rows, none = nothing(m[r], l[r]);
+            float* to = whole ? a.out + (row0 + g) * s.dv : a.parts + (part_row + g) * s.dv;
 #pragma unroll
             for (int n = 0; n < DP / 8; ++n) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float v = o[n][2 * r + e];
-                    if (SETS != 3) v += o[n][2 + e];
-                    if (SETS == 1) v += __shfl_xor_sync(0xffffffffu, v, 16);
-                    const int col = n * 8 + pair * 2 + e;
-                    if (g < kRows && col < s.dv) row[col] = v;
+                float2 u = both(SETS == 3 ? o[n][r] : add2(o[n][0], o[n][1]));
+                if (SETS == 1) {
+                    u.x += __shfl_xor_sync(0xffffffffu, u.x, 16);
+                    u.y += __shfl_xor_sync(0xffffffffu, u.y, 16);
+                }
+                const int col = n * 8 + pair * 2;
+                if (mine && col < s.dv && (SETS != 1 || (n & 1) == quad >> 2)) {
+                    if (whole) u.x = none ? 0.f : u.x / l[r], u.y = none ? 0.f : u.y / l[r];
+                    to[col] = u.x;
+                    to[col + 1] = u.y;
                 }
             }
-            if (g < kRows && pair == 0) {
-                row[s.dv] = m[r];
-                row[s.dv + 1] = l[r];
+            if (mine && pair == 0 && (SETS != 1 || quad < 4)) {
+                if (!whole) a.parts_lm[part_row + g] = make_float2(l[r], m[r]);
+                else if (a.lse) a.lse[row0 + g] = log_sum(m[r], l[r]);
             }
         }
-        __syncthreads();
-        const bool whole = k0 == 0 && k1 == tiles && !a.csplits && !a.logits;
-        const int64_t unit = (int64_t)b * per_tile + in_b;
-        join_warps<kRows>(a, merge, whole ? nullptr : a.parts + (unit + c) * a.rows * c1_row(s.dv),
-                          (int64_t)b * s.hq + g0, rows);
-        __syncthreads();
-        t += k1 - k0;
-        k0 = 0;
-        if (t < t_last && ++in_b == per_tile) {
-            in_b = 0;
-            do {
-                len = checked_len(a.lens, ++b, s.cap, a.status);
-            } while (len == 0);
-            tiles = (len + kTile - 1) / kTile;
-        }
+        now.skip(a, last - start, KEYS);
     }
 }
 
 // Joins the partial rows of every query row, and adds the step's weights to
 // the scores.  Blocks [0, B hq) take a query row each: a warp takes every
-// fourth set, a lane four columns.  With scores, the others take kScoreKeys
+// eighth set, a lane four columns.  With scores, the others take kScoreKeys
 // positions of one (sequence, kv head) each: the rows' references and
 // normalisers first (a warp a row), then the logits that the pages' kernel
 // left, 2^(x - m) / L summed over the group's rows.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kScoreKeys = 1024;
 constexpr int kScoreRows = 64;    // rows whose references are held at a time
 
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendArgs a, int tile) {
-    __shared__ int64_t place_sh[4 + kJoinWarps];
-    __shared__ float sums[kJoinWarps][256];
+    __shared__ int place_sh[2 + kJoinWarps];
+    __shared__ __align__(16) float sums[kJoinWarps][256];   // (read and written four at a time)
     __shared__ float refs[kScoreRows][2];
     const View& s = a.s;
-    const int per_tile = s.hkv * a.row_tiles, dv = s.dv, ld = c1_row(dv);
+    const int per_tile = s.hkv * a.row_tiles, dv = s.dv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool score = (int)blockIdx.x >= s.B * s.hq;
     const int chunks = (s.cap + kScoreKeys - 1) / kScoreKeys;
@@ -911,42 +920,53 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
     }
     const int len = checked_len(a.lens, b, s.cap, a.status);
     if (score && key0 >= len) return;
-    grid_dependency_wait();   // the partial rows (and everything before them) are there from here on
-    const Place at = find_place<kJoinThreads>(s, a.lens, tile, per_tile, 0, a.blocks, b, a.status, place_sh);
+    const Place at = find_place<kJoinThreads>(s, a.lens, tile, per_tile, a.workers, 0, b, a.status, place_sh);
+    const Share share(max(at.total, 1), max(at.workers, 1));
     const int tiles = (len + tile - 1) / tile;
-    // sets of partial rows of query row hq: first of the pages' (one per block), then of the coreset's
-    const float *pages = nullptr, *core = nullptr;
+    // rows of partial sums of query row hq: first of the pages' (one per worker), then of the coreset's
+    int64_t page0 = 0, core0 = 0;
     int n_pages = 0, n = 0;
-    const int64_t step = (int64_t)a.rows * ld;
     auto find_sets = [&](int hq) {
         const int g = hq % s.group, in_b = hq / s.group * a.row_tiles + g / a.rows, in_unit = g % a.rows;
         n_pages = 0;
         if (tiles > 0) {
-            const int64_t t0 = at.before + (int64_t)in_b * tiles;
-            const int c0 = block_of(t0, at.total, at.blocks), c1 = block_of(t0 + tiles - 1, at.total, at.blocks);
-            if (c0 == c1 && !a.csplits && !a.logits) return false;   // finished by the block itself
-            pages = a.parts + ((int64_t)b * per_tile + in_b + c0) * step + in_unit * ld;
+            const int t0 = at.before + in_b * tiles, c0 = share.worker(t0), c1 = share.worker(t0 + tiles - 1);
+            if (c0 == c1 && !a.csplits && !a.logits) return false;   // finished by the worker itself
+            page0 = ((int64_t)b * per_tile + in_b + c0) * a.rows + in_unit;
             n_pages = c1 - c0 + 1;
         }
-        if (a.csplits) core = a.cparts + ((int64_t)b * per_tile + in_b) * a.csplits * step + in_unit * ld;
+        core0 = ((int64_t)b * per_tile + in_b) * a.csplits * a.rows + in_unit;
         n = n_pages + a.csplits;
         return true;
     };
-    auto set = [&](int i) { return i < n_pages ? pages + i * step : core + (i - n_pages) * step; };
+    auto lm = [&](int i) {
+        return i < n_pages ? a.parts_lm[page0 + (int64_t)i * a.rows] : a.cparts_lm[core0 + (int64_t)(i - n_pages) * a.rows];
+    };
+    auto row_of = [&](int i) {
+        return i < n_pages ? a.parts + (page0 + (int64_t)i * a.rows) * dv
+                           : a.cparts + (core0 + (int64_t)(i - n_pages) * a.rows) * dv;
+    };
     // a warp's reference and normaliser over all sets, in an order that the number of sets alone decides
     auto total = [&](float& m, float& l) {
         m = -CUDART_INF_F;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, set(i)[dv + 1]);
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, lm(i).y);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float ref = m == -CUDART_INF_F ? 0.f : m;
         l = 0.f;
-        for (int i = lane; i < n; i += 32) l = fmaf(ex2(set(i)[dv + 1] - ref), set(i)[dv], l);
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) {
+            const float2 v = lm(i);
+            l = fmaf(ex2(v.y - ref), v.x, l);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     };
+    const bool to_join = score || find_sets(hq0);
+    grid_dependency_wait();   // the partial rows (and everything before them) are there from here on
+    if (!to_join) return;
     if (!score) {
-        if (!find_sets(hq0)) return;
         float m, l;
         total(m, l);
         const float ref = m == -CUDART_INF_F ? 0.f : m;
@@ -955,14 +975,14 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
-#pragma unroll 4
-        for (int i = warp; i < n; i += kJoinWarps) {
-            const float* p = set(i);
-            const float f = ex2(p[dv + 1] - ref);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                if (k * 128 + lane * 4 < dv) {
-                    const float4 v = *reinterpret_cast<const float4*>(p + k * 128 + lane * 4);
+        for (int k = 0; k < 2; ++k) {
+            const int col = k * 128 + lane * 4;
+            if (col < dv)
+#pragma unroll 8
+                for (int i = warp; i < n; i += kJoinWarps) {
+                    const float f = ex2(lm(i).y - ref);
+                    const float4 v = *reinterpret_cast<const float4*>(row_of(i) + col);
                     o[k][0] = fmaf(f, v.x, o[k][0]);
                     o[k][1] = fmaf(f, v.y, o[k][1]);
                     o[k][2] = fmaf(f, v.z, o[k][2]);
@@ -1023,7 +1043,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
 // each.  The answer (and the kernel's shared-memory limit, set before it is
 // asked for) is kept per kernel, device and size: the calls cost more than a
 // short attention's kernels do.
-wc_status resident_blocks(const void* kern, int smem, int* out) {
+wc_status resident_blocks(const void* kern, int threads, int smem, int* out) {
     struct Entry { const void* kern; int dev, smem, blocks; };
     constexpr int kEntries = 256;
     static Entry table[kEntries];
@@ -1049,7 +1069,7 @@ wc_status resident_blocks(const void* kern, int smem, int* out) {
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit - (int)fa.sharedSizeBytes) !=
             cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) != cudaSuccess || per_sm < 1)
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1)
         return WC_ERR_CUDA;
     *out = nsm * per_sm;
     if (n < kEntries) {
@@ -1060,15 +1080,17 @@ wc_status resident_blocks(const void* kern, int smem, int* out) {
 }
 
 // Launches one of the page kernels (its grid: as many blocks as the GPU holds
-// at once, or one per tile where there are fewer) and the join.
-wc_status run(AttendArgs a, void (*kern)(const AttendArgs), int smem, int tile, cudaStream_t st) {
+// at once, or one per step where there are fewer) and the join.
+wc_status run(AttendArgs a, void (*kern)(const AttendArgs), int warps, int smem, int tile, cudaStream_t st) {
     int room = 0;
-    if (resident_blocks(reinterpret_cast<const void*>(kern), smem, &room) != WC_OK) return WC_ERR_CUDA;
-    const int64_t most = (int64_t)a.s.B * a.s.hkv * a.row_tiles * ((a.s.cap + tile - 1) / tile);
-    a.blocks = (int)min(most, (int64_t)min(room, kMaxBlocks));
-    const int64_t grid = a.blocks + (int64_t)a.csplits * a.s.B * a.s.hkv * a.row_tiles;
+    if (resident_blocks(reinterpret_cast<const void*>(kern), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
+    const int64_t units = (int64_t)a.s.B * a.s.hkv * a.row_tiles, most = units * ((a.s.cap + tile - 1) / tile);
+    if (most > INT32_MAX) return WC_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
+    a.blocks = (int)min((most + warps - 1) / warps, (int64_t)min(room, kMaxWorkers / warps));
+    a.workers = a.blocks * warps;
+    const int64_t grid = a.blocks + a.csplits * units;
     if (grid > INT32_MAX) return WC_ERR_UNSUPPORTED;
-    kern<<<(unsigned)grid, kThreads, smem, st>>>(a);
+    kern<<<(unsigned)grid, warps * 32, smem, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
     const int64_t chunks = (a.s.cap + kScoreKeys - 1) / kScoreKeys;
     const int64_t join = (int64_t)a.s.B * a.s.hq + (a.scores ? chunks * a.s.B * a.s.hkv : 0);
@@ -1086,26 +1108,29 @@ wc_status run(AttendArgs a, void (*kern)(const AttendArgs), int smem, int tile, 
     return cudaLaunchKernelEx(&cfg, cache_join_kernel, a, tile) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
 }
 
-template <int RG, int NT>
+template <int DP, int RG>
 wc_status run_simt(const AttendArgs& a, cudaStream_t st) {
-    int smem = SimtSmem<NT, RG>(a.s.d, a.s.dv, 4).total;
-    if (a.csplits) smem = max(smem, CoresetSmem<NT, RG>(a.s.d, a.s.dv, 4).total);
-    return a.s.dv <= 128 ? run(a, cache_attend_simt_kernel<RG, NT, 1>, smem, kWarps * NT, st)
-                         : run(a, cache_attend_simt_kernel<RG, NT, 2>, smem, kWarps * NT, st);
+    int smem = SimtSmem<DP, RG>::total;
+    if (a.csplits) smem = max(smem, CoresetSmem<8, RG, kSimtWarps>(a.s.d, a.s.dv, 4).total);
+    return run(a, cache_attend_simt_kernel<DP, RG>, kSimtWarps, smem, kSimtKeys, st);
 }
 
-template <int RG>
-wc_status by_keys(const AttendArgs& a, cudaStream_t st) {
-    // 16 keys a warp while two stages of them fit shared memory beside the rest (rows of up to 1024 bytes)
-    return (a.s.d + a.s.dv) * 4 <= 1024 ? run_simt<RG, 16>(a, st) : run_simt<RG, 8>(a, st);
+template <int DP>
+wc_status by_rows(const AttendArgs& a, cudaStream_t st) {
+    switch (a.rows) {
+        case 1: return run_simt<DP, 1>(a, st);
+        case 2: return run_simt<DP, 2>(a, st);
+        case 4: return run_simt<DP, 4>(a, st);
+        default: return run_simt<DP, 8>(a, st);
+    }
 }
 
 template <int DP, int SETS>
 wc_status run_mma(const AttendArgs& a, cudaStream_t st) {
     constexpr int rows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
-    int smem = kWarps * kMmaStages * 2 * kMmaKeys * DP * 2;
-    if (a.csplits) smem = max(smem, CoresetSmem<kCoresetKeys<DP>, rows>(a.s.d, a.s.dv, 2).total);
-    return run(a, cache_attend_mma_kernel<DP, SETS>, smem, kWarps * kMmaKeys, st);
+    int smem = kMmaWarps<DP> * MmaRing<DP>::kBytes;
+    if (a.csplits) smem = max(smem, CoresetSmem<kCoresetKeys<DP>, rows, kMmaWarps<DP>>(a.s.d, a.s.dv, 2).total);
+    return run(a, cache_attend_mma_kernel<DP, SETS>, kMmaWarps<DP>, smem, kMmaKeys, st);
 }
 
 template <int DP>
@@ -1116,16 +1141,10 @@ wc_status by_sets(const AttendArgs& a, cudaStream_t st) {
 }  // namespace
 
 wc_status launch_attend(const AttendArgs& a, cudaStream_t st) {
-    if (a.s.dtype == WC_BF16) {
-        const int w = max(a.s.d, a.s.dv);
+    const int w = max(a.s.d, a.s.dv);
+    if (a.s.dtype == WC_BF16)
         return w <= 64 ? by_sets<64>(a, st) : w <= 128 ? by_sets<128>(a, st) : by_sets<256>(a, st);
-    }
-    switch (a.rows) {
-        case 1: return by_keys<1>(a, st);
-        case 2: return by_keys<2>(a, st);
-        case 4: return by_keys<4>(a, st);
-        default: return by_keys<8>(a, st);
-    }
+    return w <= 64 ? by_rows<64>(a, st) : w <= 128 ? by_rows<128>(a, st) : by_rows<256>(a, st);
 }
 
 }  // namespace cache
