@@ -47,17 +47,22 @@ wc_status make_view(const wc_cache* in, View* o) {
     o->dtype = c.dtype; o->esize = c.dtype == WC_BF16 ? 2 : 4;
     o->beta = c.scale > 0.f ? (double)c.scale : 1.0 / sqrt((double)c.d);
     o->table = nullptr;
+    int64_t k_page = c.k_page, k_token = c.k_token, v_page = c.v_page, v_token = c.v_token;
+    o->k_head = c.k_head;
+    o->v_head = c.v_head;
     if (!c.k_page && !c.k_head && !c.k_token && !c.v_page && !c.v_head && !c.v_token) {
-        o->k_token = c.d; o->k_head = (int64_t)c.page * c.d; o->k_page = c.hkv * o->k_head;
-        o->v_token = c.dv; o->v_head = (int64_t)c.page * c.dv; o->v_page = c.hkv * o->v_head;
+        k_token = c.d; o->k_head = (int64_t)c.page * c.d; k_page = c.hkv * o->k_head;
+        v_token = c.dv; o->v_head = (int64_t)c.page * c.dv; v_page = c.hkv * o->v_head;
     } else {
         if (!strides_ok(c, c.d, o->esize, c.k_page, c.k_head, c.k_token)) return WC_ERR_INVALID;
         if (!strides_ok(c, c.dv, o->esize, c.v_page, c.v_head, c.v_token)) return WC_ERR_INVALID;
-        o->k_page = c.k_page; o->k_head = c.k_head; o->k_token = c.k_token;
-        o->v_page = c.v_page; o->v_head = c.v_head; o->v_token = c.v_token;
     }
-    o->k_page *= o->esize; o->k_head *= o->esize; o->k_token *= o->esize;
-    o->v_page *= o->esize; o->v_head *= o->esize; o->v_token *= o->esize;
+    const int64_t most = 0xffffffffll / o->esize;   // the kernels multiply 32 bits by 32
+    if (k_page > most || k_token > most || v_page > most || v_token > most) return WC_ERR_UNSUPPORTED;
+    o->k_page = (uint32_t)(k_page * o->esize); o->k_token = (uint32_t)(k_token * o->esize);
+    o->v_page = (uint32_t)(v_page * o->esize); o->v_token = (uint32_t)(v_token * o->esize);
+    o->k_head *= o->esize;
+    o->v_head *= o->esize;
     return WC_OK;
 }
 
@@ -184,8 +189,8 @@ __global__ void __launch_bounds__(kCopyThreads) cache_append_kernel(const Append
                 if (pg >= 0) {
                     r.ks = a.K + b * a.k_batch + h * a.k_head + j * a.k_row;
                     r.vs = a.V + b * a.v_batch + h * a.v_head + j * a.v_row;
-                    r.kd = a.kp + pg * s.k_page + h * s.k_head + slot * s.k_token;
-                    r.vd = a.vp + pg * s.v_page + h * s.v_head + slot * s.v_token;
+                    r.kd = a.kp + (int64_t)pg * s.k_page + h * s.k_head + (int64_t)slot * s.k_token;
+                    r.vd = a.vp + (int64_t)pg * s.v_page + h * s.v_head + (int64_t)slot * s.v_token;
                     r.ok = true;
                     if (a.scores) a.scores[((int64_t)b * s.hkv + h) * s.cap + at] = 0.f;
                 }
@@ -510,10 +515,10 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArg
         const int at = a.idx[((int64_t)b * s.hkv + h) * a.keep + j], tp = page_of(s, at), slot = at - tp * s.page;
         const int to = page_of(s, j), to_slot = j - to * s.page;
         const int64_t from_page = s.table[(int64_t)b * s.max_pages + tp], to_page = a.into[(int64_t)b * s.max_pages + to];
-        r.ks = a.kp + from_page * s.k_page + h * s.k_head + slot * s.k_token;
-        r.vs = a.vp + from_page * s.v_page + h * s.v_head + slot * s.v_token;
-        r.kd = a.kp + to_page * s.k_page + h * s.k_head + to_slot * s.k_token;
-        r.vd = a.vp + to_page * s.v_page + h * s.v_head + to_slot * s.v_token;
+        r.ks = a.kp + from_page * s.k_page + h * s.k_head + (int64_t)slot * s.k_token;
+        r.vs = a.vp + from_page * s.v_page + h * s.v_head + (int64_t)slot * s.v_token;
+        r.kd = a.kp + to_page * s.k_page + h * s.k_head + (int64_t)to_slot * s.k_token;
+        r.vd = a.vp + to_page * s.v_page + h * s.v_head + (int64_t)to_slot * s.v_token;
         r.ok = true;
     }
     copy_rows(r, s.d * s.esize / 16, s.dv * s.esize / 16);

@@ -90,120 +90,130 @@ struct Walk {
         h = unit / a.row_tiles;
         rt = unit - h * a.row_tiles;
     }
-    // past n tiles of this unit, to the next unit behind its last one
-    __device__ __forceinline__ void skip(const AttendArgs& a, int n, int tile) {
+    // past n tiles of this unit, to the next unit behind its last one (true then)
+    __device__ __forceinline__ bool skip(const AttendArgs& a, int n, int tile) {
         left -= n;
         k += n;
-        if (left <= 0 || k < tiles) return;
+        if (left <= 0 || k < tiles) return false;
         k = 0;
-        if (++rt < a.row_tiles) return;
-        rt = 0;
-        if (++h < a.s.hkv) return;
-        h = 0;
-        do len = checked_len(a.lens, ++b, a.s.cap, a.status);
-        while (len == 0);
-        tiles = (len + tile - 1) / tile;
+        if (++rt == a.row_tiles) {
+            rt = 0;
+            if (++h == a.s.hkv) {
+                h = 0;
+                do len = checked_len(a.lens, ++b, a.s.cap, a.status);
+                while (len == 0);
+                tiles = (len + tile - 1) / tile;
+            }
+        }
+        return true;
     }
-    __device__ __forceinline__ void next(const AttendArgs& a, int tile) { skip(a, 1, tile); }
 };
 
 // A warp's ring of stages in shared memory.  A stage holds the key rows of one
-// step's KEYS keys, then their value rows, each row 16 bytes longer than DP
-// elements, so that eight rows at one column lie in eight different bank groups.
-// Rows come by 16-byte asynchronous copies, a row to 32 lanes or fewer.  Where
-// a page holds whole steps, a lane's sources are one base and a fixed stride
-// apart, and no copy needs an address of its own beyond an addition: the
-// kernels are bound by instruction issue before they are by memory (one bulk
-// copy a row, issued lane by lane, cost 16 cycles each and 4.4 TB/s in all).
+// step's KEYS keys, then their value rows, of DP elements each; the 16-byte
+// pieces of a row stand XOR-swizzled by the row, so that eight rows at one
+// column lie in eight different bank groups.  (Rows padded by 16 bytes would do
+// that too, but pieces that arrive at unaligned 128-byte groups take two writes
+// each: 8 % slower throughout.)  Rows come by 16-byte asynchronous copies, a row
+// to 32 lanes or fewer.  Where a page holds whole steps, a lane's sources are
+// one base and a fixed stride apart, and no copy needs more than an addition
+// for its address: with addresses of their own the copies took half of all
+// instructions, and one bulk copy a row, issued lane by lane, 16 cycles each.
 template <int KEYS, int DP, int ESIZE, int STAGES>
 struct Ring {
-    static constexpr int kRow = DP * ESIZE + 16, kStage = 2 * KEYS * kRow;
+    static constexpr int kRow = DP * ESIZE, kStage = 2 * KEYS * kRow;
     static constexpr int kBytes = STAGES * kStage;
     static constexpr int kChunks = DP * ESIZE / 16;                  // pieces of a row
     static constexpr int kPass = kChunks < 32 ? 32 / kChunks : 1;    // rows of one warp-wide copy
     static constexpr int kParts = kChunks < 32 ? 1 : kChunks / 32;   // copies a row takes
-    uint32_t mem;            // the ring, and this lane's piece of its first row
+    uint32_t mem;            // the ring at this lane's first row
     int row0, ch;            // this lane's first row of a step and its piece
     bool whole;              // a page holds whole steps
-    const char *k, *v;       // the next step: this lane's first sources (whole), or its key's row
-    uint32_t live;           // and a bit for each of its keys that is there
+    const char *k, *v;       // this lane's places in page 0 of the unit at hand
+    // the next step: its page as the table has it (of this lane's key, where not whole), the slot in it, the keys
+    int page, slot, keys;
 
     __device__ __forceinline__ void init(const AttendArgs& a, char* memory) {
         const View& s = a.s;
         const int lane = threadIdx.x & 31;
         row0 = lane / kChunks % kPass;
         ch = lane % (kChunks < 32 ? kChunks : 32);
-        mem = (uint32_t)__cvta_generic_to_shared(memory) + row0 * kRow + ch * 16;
+        mem = (uint32_t)__cvta_generic_to_shared(memory) + row0 * kRow;
         whole = s.page % KEYS == 0;
-        k = v = nullptr;
-        live = 0;
         // columns past the width are never copied and count as zeros
         if (s.d < DP || s.dv < DP)
             for (int i = lane; i < kBytes / 16; i += 32) reinterpret_cast<uint4*>(memory)[i] = make_uint4(0, 0, 0, 0);
         __syncwarp();
     }
-    // Where the step at w comes from.
+    // Where this lane's piece of a row stands in it.
+    __device__ __forceinline__ uint32_t place(int row) const { return (ch ^ (row & 7)) * 16; }
+    // The unit that w is in.
+    __device__ __forceinline__ void enter(const AttendArgs& a, const Walk& w) {
+        const View& s = a.s;
+        k = a.kp + w.h * s.k_head + (whole ? row0 * (int64_t)s.k_token + ch * 16 : 0);
+        v = a.vp + w.h * s.v_head + (whole ? row0 * (int64_t)s.v_token + ch * 16 : 0);
+    }
+    // Reads the table for the step at w; nothing here waits for the entry, so
+    // that it is on its way while the step before is computed.
     __device__ __forceinline__ void locate(const AttendArgs& a, const Walk& w) {
         const View& s = a.s;
-        live = 0;
+        keys = 0;
         if (w.left <= 0) return;
         const int first = w.k * KEYS, key = first + (whole ? 0 : (threadIdx.x & 31) % KEYS);
-        bool valid = false;
-        if (key < w.len) {
-            const int tp = page_of(s, key), slot = key - tp * s.page + (whole ? row0 : 0);
-            const int pg = checked_page(s, s.table, w.b, tp, a.status);
-            if (pg >= 0) {
-                k = a.kp + pg * s.k_page + w.h * s.k_head + slot * s.k_token + (whole ? ch * 16 : 0);
-                v = a.vp + pg * s.v_page + w.h * s.v_head + slot * s.v_token + (whole ? ch * 16 : 0);
-                valid = true;
-            }
-        }
-        const uint32_t all = (uint32_t)((1ull << KEYS) - 1);
-        if (whole) live = !valid ? 0u : w.len - first >= KEYS ? all : (1u << (w.len - first)) - 1;
-        else live = __ballot_sync(0xffffffffu, valid) & all;
+        keys = min(KEYS, w.len - first);
+        const int tp = page_of(s, min(key, w.len - 1));
+        slot = key - tp * s.page;
+        page = __ldg(s.table + (int64_t)w.b * s.max_pages + tp);
     }
-    // Starts the copies of the located step; a value row that is not there is
-    // filled with zeros (its weight is 0, and 0 times what lay there may not be).
-    __device__ __forceinline__ void fetch(const AttendArgs& a, int stage) {
+    // Starts the copies of the located step and returns a bit for each key that
+    // is there.  A value row that is not is filled with zeros (its weight is 0,
+    // and 0 times what lay there may not be).
+    __device__ __forceinline__ uint32_t fetch(const AttendArgs& a, int stage) {
         const View& s = a.s;
         const uint32_t kd = mem + stage * kStage, vd = kd + KEYS * kRow;
         const int ck = s.d * ESIZE / 16, cv = s.dv * ESIZE / 16;
-        if (whole && live == (uint32_t)((1ull << KEYS) - 1)) {
-            const char *ks = k, *vs = v;
-            const int64_t kstep = kPass * s.k_token, vstep = kPass * s.v_token;
+        const uint32_t all = (uint32_t)((1ull << KEYS) - 1);
+        const bool good = (unsigned)page < (unsigned)s.n_pages;
+        const uint32_t pg = good ? page : 0;
+        const char* ks = k + (uint64_t)pg * s.k_page + (uint64_t)(uint32_t)slot * s.k_token;
+        const char* vs = v + (uint64_t)pg * s.v_page + (uint64_t)(uint32_t)slot * s.v_token;
+        if (whole && good && keys == KEYS) {
 #pragma unroll
             for (int i = 0; i < KEYS / kPass; ++i) {
 #pragma unroll
                 for (int p = 0; p < kParts; ++p) {
-                    if (ch + p * 32 < ck) cp_async16(kd + i * kPass * kRow + p * 512, ks + p * 512);
-                    if (ch + p * 32 < cv) cp_async16(vd + i * kPass * kRow + p * 512, vs + p * 512);
+                    const uint32_t off = i * kPass * kRow + p * 512 + place(i * kPass + row0);
+                    cp_async16_if(ch + p * 32 < ck, kd + off, ks + p * 512);
+                    cp_async16_if(ch + p * 32 < cv, vd + off, vs + p * 512);
                 }
-                ks += kstep;
-                vs += vstep;
+                ks += kPass * (uint64_t)s.k_token;
+                vs += kPass * (uint64_t)s.v_token;
             }
-            return;
+            return all;
         }
+        if (!good) record_status(a.status, WC_ERR_BOUNDS);
+        uint32_t live = keys >= KEYS ? all : (1u << keys) - 1;
+        if (whole) live = good ? live : 0u;
+        else live &= __ballot_sync(0xffffffffu, good);
+#pragma unroll 1
         for (int i = 0; i < KEYS / kPass; ++i) {
             const int row = i * kPass + row0;
-            const char *ks, *vs;
-            if (whole) {
-                ks = k + i * kPass * s.k_token;
-                vs = v + i * kPass * s.v_token;
-            } else {
-                ks = shfl_ptr(k, row) + ch * 16;
-                vs = shfl_ptr(v, row) + ch * 16;
+            const char *kr = ks + i * kPass * (int64_t)s.k_token, *vr = vs + i * kPass * (int64_t)s.v_token;
+            if (!whole) {
+                kr = shfl_ptr(ks, row) + ch * 16;
+                vr = shfl_ptr(vs, row) + ch * 16;
             }
             const bool there = (live >> row) & 1;
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
-                if (there && ch + p * 32 < ck) cp_async16(kd + i * kPass * kRow + p * 512, ks + p * 512);
-                if (ch + p * 32 < cv) {
-                    const uint32_t to = vd + i * kPass * kRow + p * 512;
-                    if (there) cp_async16(to, vs + p * 512);
-                    else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
-                }
+                const uint32_t off = i * kPass * kRow + p * 512 + place(row);
+                cp_async16_if(there && ch + p * 32 < ck, kd + off, kr + p * 512);
+                cp_async16_if(there && ch + p * 32 < cv, vd + off, vr + p * 512);
+                if (!there && ch + p * 32 < cv)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vd + off), "r"(0) : "memory");
             }
         }
+        return live;
     }
 };
 
@@ -437,14 +447,15 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
     ring.init(a, mem);
     uint32_t masks = 0;   // the live keys of the steps in the ring, a byte each, the next one lowest after a fetch
     auto fetch = [&](int stage) {   // the next step's copies; where the one after it is
-        masks = masks >> 8 | ring.live << 8;
+        masks >>= 8;
         if (ahead.left > 0) {
-            ring.fetch(a, stage);
-            ahead.next(a, KEYS);
-            ring.locate(a, ahead);   // (a step early: the table entry is there when it is used)
+            masks |= ring.fetch(a, stage) << 8;
+            if (ahead.skip(a, 1, KEYS)) ring.enter(a, ahead);
+            ring.locate(a, ahead);
         }
         cp_async_commit();
     };
+    ring.enter(a, ahead);
     ring.locate(a, ahead);
     fetch(0);
     const int key = lane % KEYS, part = lane / KEYS;
@@ -481,7 +492,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
 #pragma unroll 8
         for (int i = 0; i < kChunks / 4; ++i) {
             const int ch = part + 4 * i;
-            const float4 k4 = *reinterpret_cast<const float4*>(krows + key * SimtRing<DP>::kRow + ch * 16);
+            const float4 k4 = *reinterpret_cast<const float4*>(krows + key * SimtRing<DP>::kRow + (ch ^ key) * 16);
 #pragma unroll
             for (int g = 0; g < RG; ++g) {
                 const float4 q4 = *reinterpret_cast<const float4*>(q + g * DP + ch * 4);
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
                 const int ch = (kGroups > 1 ? lane % kChunks : lane) + n * 32;
-                const float4 y = *reinterpret_cast<const float4*>(vrows + j * SimtRing<DP>::kRow + ch * 16);
+                const float4 y = *reinterpret_cast<const float4*>(vrows + j * SimtRing<DP>::kRow + (ch ^ (j & 7)) * 16);
 #pragma unroll
                 for (int g = 0; g < RG; ++g) {
                     o[g][n * 4] = fmaf(w[g], y.x, o[g][n * 4]);
@@ -688,14 +699,15 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
     ring.init(a, mem);
     uint64_t masks = 0;   // the live keys of the steps in the ring, 16 bits each, the next one lowest after a fetch
     auto fetch = [&](int stage) {   // the next step's copies; where the one after it is
-        masks = masks >> 16 | (uint64_t)ring.live << (16 * (kStages - 1));
+        masks >>= 16;
         if (ahead.left > 0) {
-            ring.fetch(a, stage);
-            ahead.next(a, KEYS);
-            ring.locate(a, ahead);   // (a step early: the table entry is there when it is used)
+            masks |= (uint64_t)ring.fetch(a, stage) << (16 * (kStages - 1));
+            if (ahead.skip(a, 1, KEYS)) ring.enter(a, ahead);
+            ring.locate(a, ahead);
         }
         cp_async_commit();
     };
+    ring.enter(a, ahead);
     ring.locate(a, ahead);
 #pragma unroll 1
     for (int p = 0; p < kStages - 1; ++p) fetch(p);
@@ -752,11 +764,11 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
             for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
         {
             const int row = (lane & 7) + ((lane >> 4) << 3);
-            const uint32_t base = kd + row * kRow + ((lane >> 3) & 1) * 16;
+            const uint32_t base = kd + row * kRow;
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
                 uint32_t f[4];
-                ldmatrix4(f, base + k * 32);
+                ldmatrix4(f, base + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
                 if (SETS == 3) {
                     mma16816(x[0], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[0], f[1]);
                     mma16816(x[1], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[2], f[3]);
@@ -817,7 +829,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         // values
         {
             const int row = lane & 15;
-            const uint32_t base = vd + row * kRow + (lane >> 4) * 16;
+            const uint32_t base = vd + row * kRow;
             uint32_t p0 = 0, p1 = 0, p2 = 0, p3 = 0;
             if (SETS == 1) {   // rows 0-3: term 0, 8-11: term 1, 4-7: term 2, 12-15: nothing
                 const bool up = quad < 4;
@@ -827,7 +839,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
 #pragma unroll
             for (int n = 0; n < DP / 16; ++n) {
                 uint32_t f[4];
-                ldmatrix4t(f, base + n * 32);
+                ldmatrix4t(f, base + (((2 * n + (lane >> 4)) ^ (row & 7)) << 4));
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     // The product of the 16 keys by itself, then an ordinary fp32 addition: the

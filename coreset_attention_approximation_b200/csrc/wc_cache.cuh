@@ -18,7 +18,8 @@ struct View {
     int page, n_pages, max_pages, cap;   // cap = max_pages * page
     uint32_t page_mul; int page_shift;   // t / page = t * page_mul >> page_shift for 0 <= t < 2^31
     int dtype, esize;
-    int64_t k_page, k_head, k_token, v_page, v_head, v_token;   // bytes
+    uint32_t k_page, k_token, v_page, v_token;   // bytes
+    int64_t k_head, v_head;
     double beta;
 };
 
@@ -95,6 +96,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ const char* shfl_ptr(const char* p, int from) {
     return reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), from));
+}
+// The same where `go`, by a predicate (never a branch).
+__device__ __forceinline__ void cp_async16_if(bool go, uint32_t dst, const void* src) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+                 "l"(src), "r"((int)go)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

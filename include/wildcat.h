@@ -298,7 +298,8 @@ typedef struct {
     float scale;        /* beta; 0 selects 1/sqrt(d) */
     int64_t k_page, k_head, k_token;  /* strides of k in elements, multiples of 16 bytes, each */
     int64_t v_page, v_head, v_token;  /* at least a row where its axis is longer than 1; all
-                                         six 0: dense pools in the order above */
+                                         six 0: dense pools in the order above.  A page or token
+                                         stride of 4 GiB or more: WC_ERR_UNSUPPORTED */
 } wc_cache;
 
 /* Workspace bytes of every cache call, with accumulation (1) or without (0);
