@@ -93,8 +93,8 @@ Layout make_layout(const View& s, bool accumulate) {
     L.status = take(256);
     L.marks = take(sizeof(int32_t) * (size_t)s.n_pages);
     L.lens = take(sizeof(int32_t) * 2 * (size_t)s.B);
-    L.parts = take((units + kMaxWorkers) * set);
-    L.parts_lm = take((units + kMaxWorkers) * lm);
+    L.parts = take((units + max_warps(s)) * set);
+    L.parts_lm = take((units + max_warps(s)) * lm);
     L.cparts = take((units + kCoresetBlocks) * set);
     L.cparts_lm = take((units + kCoresetBlocks) * lm);
     L.logits = take(accumulate ? sizeof(float) * (size_t)s.B * s.hq * s.cap : 0);
@@ -166,6 +166,8 @@ __device__ __forceinline__ void copy_rows(const RowCopy& r, int ck, int cv) {
 
 // One warp per 16 new rows of one (sequence, kv head).
 __global__ void __launch_bounds__(kCopyThreads) cache_append_kernel(const AppendArgs a) {
+    grid_dependency_wait();
+    grid_dependents_launch();
     const View& s = a.s;
     const int lane = threadIdx.x & 31, groups = (a.t + kCopyRows - 1) / kCopyRows;
     const int64_t items = (int64_t)s.B * s.hkv * groups;
@@ -626,9 +628,8 @@ wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const
     a.status = static_cast<int*>(ws);
     const int64_t items = (int64_t)a.s.B * a.s.hkv * ((t + (int64_t)kCopyRows - 1) / kCopyRows);
     const int64_t grid = (items + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
-    cache_append_kernel<<<(unsigned)(grid < 148 * 64 ? grid : 148 * 64), kCopyThreads, 0,
-                          static_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? WC_OK : WC_ERR_CUDA;
+    return launch(cache_append_kernel, grid < 148 * 64 ? grid : 148 * 64, kCopyThreads, 0,
+                  static_cast<cudaStream_t>(stream), a) ? WC_OK : WC_ERR_CUDA;
 }
 
 wc_status wc_cache_attend(const wc_cache* cache, const void* Q, int64_t q_batch, int64_t q_head, const void* k,

@@ -5,11 +5,18 @@
 // One pass over the keys and values with a running maximum per query row (in
 // log2 units, so one multiplication by beta log2(e) is folded into the query):
 // a partial result is (O, l, m) with O = sum 2^(x - m) v, l = sum 2^(x - m).
-// The key tiles of the whole batch are divided evenly over the warps
-// (wc_cache.cuh), whatever the lengths; a warp streams its tiles through a ring
+// The key tiles of the whole batch are divided over the warps (Share in
+// wc_cache.cuh), whatever the lengths; a warp streams its tiles through a ring
 // of its own in shared memory, on from one sequence or head to the next, and
-// never waits for another.  A second kernel joins a unit's partial rows in
-// order of the warps.
+// never waits for another.  The coreset is a kernel of its own that runs beside
+// it.  A last kernel joins the partial rows, in order of the stretches and of
+// the coreset's splits.
+//
+// The kernels overlap by programmatic dependent launch: each may start before
+// the one ahead of it has ended, lets the next start once it knows that the
+// stream's earlier work is complete, and waits before it reads what the one
+// ahead wrote.  The pages' kernel reads nothing of the coreset's; it waits for
+// it at its end, so that its own end means both to the join.
 #include <atomic>
 #include <mutex>
 
@@ -65,26 +72,36 @@ __device__ __forceinline__ void tile_logits(const char* krows, int k_row, const 
         for (int g = 0; g < RG; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
 }
 
-// A warp's way through its tiles: the unit (sequence b, kv head h, row tile rt)
-// and the tile k of its `tiles`.
+// A warp's way through its tiles: the stretch, the unit (sequence b, kv head h,
+// row tile rt) and the tile k of its `tiles`.
 struct Walk {
-    int left;          // tiles to go, this one included
+    int left;          // tiles to the end of the stretch, this one included
+    int stretch;
     int b, h, rt, k, tiles, len;
-    // first tile of worker c, from the place of a worker not behind it
-    __device__ __forceinline__ void start(const AttendArgs& a, const Place& at, int c, int tile) {
-        const Share share(at.total, max(at.workers, 1));
-        int t = c < at.workers ? share.first(c) : at.total;
-        left = c < at.workers ? share.first(c + 1) - t : 0;
+    // to the first tile of stretch c; pre: the tiles before every step-th sequence
+    __device__ __forceinline__ void start(const AttendArgs& a, const Share& share, const int* pre, int step, int c,
+                                          int tile) {
+        stretch = c;
+        left = 0;
         b = h = rt = k = tiles = len = 0;
-        if (left <= 0) return;
+        if (c >= share.count) return;
+        int t = share.first(c);
+        left = share.last(c) - t;
         const int per_tile = a.s.hkv * a.row_tiles;
-        t -= at.before;
-        for (b = at.b;; ++b) {
-            len = checked_len(a.lens, b, a.s.cap, a.status);
-            tiles = (len + tile - 1) / tile;
-            if (t < tiles * per_tile) break;
-            t -= tiles * per_tile;
+        int lo = 0, hi = (a.s.B + step - 1) / step;   // the last place with no more than t tiles before it
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (pre[mid] <= t) lo = mid;
+            else hi = mid;
         }
+        t -= pre[lo];
+        for (b = lo * step;; ++b) {
+            len = checked_len(a.lens, b, a.s.cap, a.status);
+            const int n = (len + tile - 1) / tile * per_tile;
+            if (t < n) break;
+            t -= n;
+        }
+        tiles = (len + tile - 1) / tile;
         const int unit = t / tiles;
         k = t - unit * tiles;
         h = unit / a.row_tiles;
@@ -106,6 +123,10 @@ struct Walk {
             }
         }
         return true;
+    }
+    // row of the unit's first partial row
+    __device__ __forceinline__ int64_t part_row(const AttendArgs& a) const {
+        return ((int64_t)(b * a.s.hkv + h) * a.row_tiles + rt + stretch) * a.rows;
     }
 };
 
@@ -295,9 +316,16 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // summed; a lane holds columns lane, lane + 32, ... and the row's last value is
 // its weight in the normaliser.  Sums in fp32 on CUDA cores: W's values cancel
 // one another, and there are few rows.
-template <typename T, int RG, int NT, int COLS, int WARPS>
-__device__ void coreset_block(const AttendArgs& a, int index, char* smem) {
+constexpr int kCoresetWarps = 4;
+
+template <typename T, int RG, int NT, int COLS>
+__global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const AttendArgs a) {
+    constexpr int WARPS = kCoresetWarps;
+    extern __shared__ __align__(128) char smem[];
+    grid_dependency_wait();
+    grid_dependents_launch();
     const View& s = a.s;
+    const int index = blockIdx.x;
     const CoresetSmem<NT, RG, WARPS> L(s.d, s.dv, sizeof(T));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* q = reinterpret_cast<float*>(smem + L.q);
@@ -425,23 +453,20 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
     constexpr int kCols = kChunks < 32 ? 1 : kChunks / 32;        // a lane's column quadruples
     using L = SimtSmem<DP, RG>;
     extern __shared__ __align__(128) char smem[];
-    __shared__ int place_sh[2 + kSimtWarps];
+    __shared__ int place_sh[1 + kSimtWarps], pre[kPlaces];
+    if (!a.csplits) grid_dependency_wait();   // (with a coreset its kernel has waited)
     grid_dependents_launch();
     const View& s = a.s;
-    if ((int)blockIdx.x >= a.blocks) {
-        coreset_block<float, RG, 8, DP / 32, kSimtWarps>(a, blockIdx.x - a.blocks, smem);
-        return;
-    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     char* mem = smem + warp * L::warp;
     float* q = reinterpret_cast<float*>(mem + L::q);
     float* p = reinterpret_cast<float*>(mem + L::p);
-    const int c = blockIdx.x * kSimtWarps + warp;
-    const Place at = find_place<kSimtWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, a.workers,
-                                                 blockIdx.x * kSimtWarps, -1, a.status, place_sh);
+    const int step = (s.B + kPlaces - 1) / kPlaces;
+    const Place at = scan_tiles<kSimtWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, -1, pre, step,
+                                                  a.status, place_sh);
+    const Share share(at.total, a.blocks * kSimtWarps);
     Walk now, ahead;
-    now.start(a, at, c, KEYS);
-    if (now.left <= 0) return;
+    now.start(a, share, pre, step, blockIdx.x * kSimtWarps + warp, KEYS);
     ahead = now;
     SimtRing<DP> ring;
     ring.init(a, mem);
@@ -464,7 +489,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
         // the share of one unit: steps now.k up to `last`
         const int rows = min(a.rows, s.group - now.rt * a.rows), g0 = now.h * s.group + now.rt * a.rows;
         const int start = now.k, last = min(now.tiles, now.k + now.left);
-        const int64_t row0 = (int64_t)now.b * s.hq + g0;
+        const int64_t row0 = (int64_t)now.b * s.hq + g0, part_row = now.part_row(a);
         const float* src = static_cast<const float*>(a.Q) + now.b * a.q_batch + (int64_t)g0 * a.q_head;
 #pragma unroll 4
         for (int i = lane; i < RG * DP; i += 32) {
@@ -479,7 +504,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
 #pragma unroll
             for (int i = 0; i < kCols * 4; ++i) o[g][i] = 0.f;
         }
-        for (int step = start; step < last; ++step) {
+        for (int at_k = start; at_k < last; ++at_k) {
         fetch(stage ^ 1);
         const uint32_t mask = masks & 0xff;
         cp_async_wait<1>();
@@ -503,7 +528,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
             }
         }
         const bool ok = (mask >> key) & 1;
-        const int pos = step * KEYS + key;
+        const int pos = at_k * KEYS + key;
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
             x[g] += __shfl_xor_sync(0xffffffffu, x[g], 8);
@@ -553,7 +578,6 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
         }
         // finished rows where the share is the whole unit, else partial rows
         const bool whole = start == 0 && last == now.tiles && !a.csplits && !a.logits;
-        const int64_t part_row = ((int64_t)(now.b * s.hkv + now.h) * a.row_tiles + now.rt + c) * a.rows;
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
 #pragma unroll
@@ -580,6 +604,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
         }
         now.skip(a, last - start, KEYS);
     }
+    if (a.csplits) grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------- tensor cores
@@ -636,11 +661,6 @@ __device__ __forceinline__ uint64_t pair_of(float x, float y) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
     return p;
 }
-__device__ __forceinline__ float2 both(uint64_t p) {
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     uint64_t p;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
@@ -656,7 +676,6 @@ constexpr int kMmaKeys = 16;     // keys of one warp's step
 // Stages of a warp's ring, and warps of a block: what fits two blocks an SM (one for the widest rows).
 template <int DP> constexpr int kMmaStages = DP > 128 ? 2 : 3;
 template <int DP> constexpr int kMmaWarps = DP > 128 ? 6 : 4;
-template <int DP> constexpr int kCoresetKeys = DP > 128 ? 8 : 16;   // (two stages of wider rows leave too little room)
 
 template <int DP> using MmaRing = Ring<kMmaKeys, DP, 2, kMmaStages<DP>>;
 
@@ -677,21 +696,18 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
     constexpr int kStages = kMmaStages<DP>, kBlockWarps = kMmaWarps<DP>;
     constexpr int kMine = SETS == 3 ? 2 : 1;               // rows of a lane
     extern __shared__ __align__(128) char smem[];
-    __shared__ int place_sh[2 + kBlockWarps];
+    __shared__ int place_sh[1 + kBlockWarps], pre[kPlaces];
+    if (!a.csplits) grid_dependency_wait();   // (with a coreset its kernel has waited)
     grid_dependents_launch();
     const View& s = a.s;
-    if ((int)blockIdx.x >= a.blocks) {
-        coreset_block<bf16, kRows, kCoresetKeys<DP>, DP / 32, kBlockWarps>(a, blockIdx.x - a.blocks, smem);
-        return;
-    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane >> 2, pair = lane & 3;           // fragment row and column pair
-    const int c = blockIdx.x * kBlockWarps + warp;
-    const Place at = find_place<kBlockWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, a.workers,
-                                                  blockIdx.x * kBlockWarps, -1, a.status, place_sh);
+    const int step = (s.B + kPlaces - 1) / kPlaces;
+    const Place at = scan_tiles<kBlockWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, -1, pre, step,
+                                                  a.status, place_sh);
+    const Share share(at.total, a.blocks * kBlockWarps);
     Walk now, ahead;
-    now.start(a, at, c, KEYS);
-    if (now.left <= 0) return;
+    now.start(a, share, pre, step, blockIdx.x * kBlockWarps + warp, KEYS);
     ahead = now;
     MmaRing<DP> ring;
     char* mem = smem + warp * MmaRing<DP>::kBytes;
@@ -716,7 +732,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         // the share of one unit: steps now.k up to `last`
         const int rows = min(a.rows, s.group - now.rt * a.rows), g0 = now.h * s.group + now.rt * a.rows;
         const int start = now.k, last = min(now.tiles, now.k + now.left);
-        const int64_t row0 = (int64_t)now.b * s.hq + g0;
+        const int64_t row0 = (int64_t)now.b * s.hq + g0, part_row = now.part_row(a);
         // Query fragments, as they are (the logits are scaled in fp32): rows
         // quad and, where the rows are not copies, quad + 8.
         uint32_t q[DP / 16][SETS == 3 ? 4 : 2];
@@ -750,7 +766,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = 0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
-        for (int step = start; step < last; ++step) {
+        for (int at_k = start; at_k < last; ++at_k) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
         const uint32_t kd = stages + stage * MmaRing<DP>::kStage, vd = kd + KEYS * kRow;
@@ -792,7 +808,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
                 for (int e = 0; e < 4; ++e)
                     if (!((mask >> (e / 2 * 8 + pair * 2 + e % 2)) & 1)) y[e] = -CUDART_INF_F;
             if (a.logits && quad + 8 * r < rows) {
-                const int pos = step * KEYS;
+                const int pos = at_k * KEYS;
                 float* to = a.logits + (row0 + quad + 8 * r) * s.cap + pos;
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
@@ -868,82 +884,121 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         }
         // finished rows where the share is the whole unit, else partial rows
         const bool whole = start == 0 && last == now.tiles && !a.csplits && !a.logits;
-        const int64_t part_row = ((int64_t)(now.b * s.hkv + now.h) * a.row_tiles + now.rt + c) * a.rows;
+        // The sums go through the stage that was read last (free until the next fetch): pairs of columns at
+        // row quad (quad + 8), XOR-swizzled, then out in 16-byte pieces.  Straight from the fragments the
+        // code is five times as long, and a warp that runs it once waits for its instructions.
+        float* out_sh = reinterpret_cast<float*>(mem + (stage == 0 ? kStages - 1 : stage - 1) * MmaRing<DP>::kStage);
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+            for (int r = 0; r < kMine; ++r)
+                *reinterpret_cast<uint64_t*>(out_sh + (quad + 8 * r) * DP + ((n ^ quad) * 4 + pair) * 2) =
+                    SETS == 3 ? o[n][r] : add2(o[n][0], o[n][1]);
 #pragma unroll
         for (int r = 0; r < kMine; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            // where rows 4 to 7 are copies, their lanes write every other pair of columns
-            const int g = SETS == 1 ? quad & 3 : quad + 8 * r;
-            const bool mine = g < rows, none = nothing(m[r], l[r]);
-            float* to = whole ? a.out + (row0 + g) * s.dv : a.parts + (part_row + g) * s.dv;
-#pragma unroll
-            for (int n = 0; n < DP / 8; ++n) {
-                float2 u = both(SETS == 3 ? o[n][r] : add2(o[n][0], o[n][1]));
-                if (SETS == 1) {
-                    u.x += __shfl_xor_sync(0xffffffffu, u.x, 16);
-                    u.y += __shfl_xor_sync(0xffffffffu, u.y, 16);
-                }
-                const int col = n * 8 + pair * 2;
-                if (mine && col < s.dv && (SETS != 1 || (n & 1) == quad >> 2)) {
-                    if (whole) u.x = none ? 0.f : u.x / l[r], u.y = none ? 0.f : u.y / l[r];
-                    to[col] = u.x;
-                    to[col + 1] = u.y;
-                }
-            }
-            if (mine && pair == 0 && (SETS != 1 || quad < 4)) {
+            const int g = quad + 8 * r;
+            if (pair == 0 && g < rows) {
                 if (!whole) a.parts_lm[part_row + g] = make_float2(l[r], m[r]);
                 else if (a.lse) a.lse[row0 + g] = log_sum(m[r], l[r]);
             }
         }
+        __syncwarp();
+        const int c4 = s.dv / 4, pieces = rows * c4;
+        float* to = whole ? a.out + row0 * s.dv : a.parts + part_row * s.dv;
+#pragma unroll 1
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            const int i = min(i0 + lane, pieces - 1), g = i / c4, c = i - g * c4;
+            auto piece = [&](int row) {
+                return *reinterpret_cast<const float4*>(out_sh + row * DP + ((c / 2 ^ (row & 7)) * 4 + (c & 1) * 2) * 2);
+            };
+            float4 v = piece(g);
+            if (SETS == 1) {   // the copies of the rows carried the third term
+                const float4 u = piece(g + 4);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
+            if (whole) {
+                float sum = __shfl_sync(0xffffffffu, l[0], (g & 7) * 4), top = __shfl_sync(0xffffffffu, m[0], (g & 7) * 4);
+                if (SETS == 3) {
+                    const float sum1 = __shfl_sync(0xffffffffu, l[kMine - 1], (g & 7) * 4);
+                    const float top1 = __shfl_sync(0xffffffffu, m[kMine - 1], (g & 7) * 4);
+                    if (g >= 8) sum = sum1, top = top1;
+                }
+                const bool none = nothing(top, sum);
+                v.x = none ? 0.f : v.x / sum, v.y = none ? 0.f : v.y / sum;
+                v.z = none ? 0.f : v.z / sum, v.w = none ? 0.f : v.w / sum;
+            }
+            if (i0 + lane < pieces) {
+                float* p = to + (int64_t)g * s.dv + c * 4;   // (out need not be aligned to more than a value)
+                if (whole) p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+                else *reinterpret_cast<float4*>(p) = v;
+            }
+        }
+        __syncwarp();
+        if (s.d < DP || s.dv < DP) {   // columns past the width are zeros again
+            for (int i = lane; i < MmaRing<DP>::kStage / 16; i += 32)
+                reinterpret_cast<uint4*>(out_sh)[i] = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+        }
         now.skip(a, last - start, KEYS);
     }
+    if (a.csplits) grid_dependency_wait();
 }
 
 // Joins the partial rows of every query row, and adds the step's weights to
-// the scores.  Blocks [0, B hq) take a query row each: a warp takes every
-// eighth set, a lane four columns.  With scores, the others take kScoreKeys
-// positions of one (sequence, kv head) each: the rows' references and
-// normalisers first (a warp a row), then the logits that the pages' kernel
-// left, 2^(x - m) / L summed over the group's rows.
+// the scores.  The first blocks take `cols` columns of a query row each: the
+// sets' weights 2^(m - M) into shared memory, a set a thread, then the sums,
+// four columns a thread and the sets spread over the rest (there are up to
+// hundreds of sets and few rows, and what counts is the loads in flight).  With
+// scores, the others take kScoreKeys positions of one (sequence, kv head) each:
+// the rows' references and normalisers first (a warp a row), then the logits
+// that the pages' kernel left, 2^(x - m) / L summed over the group's rows.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kScoreKeys = 1024;
+constexpr int kJoinSets = 1024;   // sets whose weights are held at a time
+constexpr int kScoreKeys = 2048;
 constexpr int kScoreRows = 64;    // rows whose references are held at a time
 
-__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendArgs a, int tile) {
-    __shared__ int place_sh[2 + kJoinWarps];
-    __shared__ __align__(16) float sums[kJoinWarps][256];   // (read and written four at a time)
+__global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const AttendArgs a, int tile, int warps, int cols) {
+    __shared__ int place_sh[1 + kJoinWarps];
+    __shared__ __align__(16) float4 sums[kJoinThreads];
+    __shared__ float weight[kJoinSets];
+    __shared__ float red[kJoinWarps];
     __shared__ float refs[kScoreRows][2];
     const View& s = a.s;
-    const int per_tile = s.hkv * a.row_tiles, dv = s.dv;
+    const int per_tile = s.hkv * a.row_tiles, dv = s.dv, slices = (dv + cols - 1) / cols;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool score = (int)blockIdx.x >= s.B * s.hq;
+    const int row_blocks = s.B * s.hq * slices;
+    const bool score = (int)blockIdx.x >= row_blocks;
     const int chunks = (s.cap + kScoreKeys - 1) / kScoreKeys;
-    int b, hq0, key0 = 0;
+    int b, hq0, key0 = 0, col0 = 0;
     if (!score) {
-        b = blockIdx.x / s.hq;
-        hq0 = blockIdx.x % s.hq;
+        const int row = blockIdx.x / slices;
+        col0 = (blockIdx.x - row * slices) * cols;
+        b = row / s.hq;
+        hq0 = row - b * s.hq;
     } else {
-        const int i = blockIdx.x - s.B * s.hq;
-        b = i / chunks / s.hkv;
-        hq0 = i / chunks % s.hkv * s.group;
-        key0 = i % chunks * kScoreKeys;
+        const int i = blockIdx.x - row_blocks, unit = i / chunks;
+        b = unit / s.hkv;
+        hq0 = (unit - b * s.hkv) * s.group;
+        key0 = (i - unit * chunks) * kScoreKeys;
     }
     const int len = checked_len(a.lens, b, s.cap, a.status);
     if (score && key0 >= len) return;
-    const Place at = find_place<kJoinThreads>(s, a.lens, tile, per_tile, a.workers, 0, b, a.status, place_sh);
-    const Share share(max(at.total, 1), max(at.workers, 1));
+    const Place at = scan_tiles<kJoinThreads>(s, a.lens, tile, per_tile, b, nullptr, 1, a.status, place_sh);
+    const Share share(at.total, warps);
     const int tiles = (len + tile - 1) / tile;
-    // rows of partial sums of query row hq: first of the pages' (one per worker), then of the coreset's
+    // rows of partial sums of query row hq: first of the pages' (one per stretch), then of the coreset's
     int64_t page0 = 0, core0 = 0;
     int n_pages = 0, n = 0;
     auto find_sets = [&](int hq) {
-        const int g = hq % s.group, in_b = hq / s.group * a.row_tiles + g / a.rows, in_unit = g % a.rows;
+        const int h = hq / s.group, g = hq - h * s.group, rt = g / a.rows, in_unit = g - rt * a.rows;
+        const int in_b = h * a.row_tiles + rt;
         n_pages = 0;
         if (tiles > 0) {
-            const int t0 = at.before + in_b * tiles, c0 = share.worker(t0), c1 = share.worker(t0 + tiles - 1);
-            if (c0 == c1 && !a.csplits && !a.logits) return false;   // finished by the worker itself
+            const int t0 = at.before + in_b * tiles, c0 = share.of(t0), c1 = share.of(t0 + tiles - 1);
+            if (c0 == c1 && !a.csplits && !a.logits) return false;   // finished by the warp itself
             page0 = ((int64_t)b * per_tile + in_b + c0) * a.rows + in_unit;
             n_pages = c1 - c0 + 1;
         }
@@ -951,70 +1006,76 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
         n = n_pages + a.csplits;
         return true;
     };
-    auto lm = [&](int i) {
-        return i < n_pages ? a.parts_lm[page0 + (int64_t)i * a.rows] : a.cparts_lm[core0 + (int64_t)(i - n_pages) * a.rows];
-    };
-    auto row_of = [&](int i) {
-        return i < n_pages ? a.parts + (page0 + (int64_t)i * a.rows) * dv
-                           : a.cparts + (core0 + (int64_t)(i - n_pages) * a.rows) * dv;
-    };
-    // a warp's reference and normaliser over all sets, in an order that the number of sets alone decides
-    auto total = [&](float& m, float& l) {
-        m = -CUDART_INF_F;
-#pragma unroll 4
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, lm(i).y);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ref = m == -CUDART_INF_F ? 0.f : m;
-        l = 0.f;
-#pragma unroll 4
-        for (int i = lane; i < n; i += 32) {
-            const float2 v = lm(i);
-            l = fmaf(ex2(v.y - ref), v.x, l);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    auto lm = [&](int i) {   // (normaliser, reference) of a set
+        return *(i < n_pages ? a.parts_lm + page0 + (int64_t)i * a.rows : a.cparts_lm + core0 + (int64_t)(i - n_pages) * a.rows);
     };
     const bool to_join = score || find_sets(hq0);
     grid_dependency_wait();   // the partial rows (and everything before them) are there from here on
     if (!to_join) return;
     if (!score) {
-        float m, l;
-        total(m, l);
+        // the maximum over all sets
+        float m = -CUDART_INF_F;
+        for (int i = threadIdx.x; i < n; i += kJoinThreads) m = fmaxf(m, lm(i).y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) red[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[w]);
         const float ref = m == -CUDART_INF_F ? 0.f : m;
-        float o[2][4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int col = k * 128 + lane * 4;
-            if (col < dv)
-#pragma unroll 8
-                for (int i = warp; i < n; i += kJoinWarps) {
-                    const float f = ex2(lm(i).y - ref);
-                    const float4 v = *reinterpret_cast<const float4*>(row_of(i) + col);
-                    o[k][0] = fmaf(f, v.x, o[k][0]);
-                    o[k][1] = fmaf(f, v.y, o[k][1]);
-                    o[k][2] = fmaf(f, v.z, o[k][2]);
-                    o[k][3] = fmaf(f, v.w, o[k][3]);
+        const int quads = cols / 4, groups = kJoinThreads / quads, q = threadIdx.x % quads, sg = threadIdx.x / quads;
+        const int col = col0 + q * 4;
+        const bool in = col < dv && sg < groups;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        for (int i0 = 0; i0 < n; i0 += kJoinSets) {
+            const int held = min(kJoinSets, n - i0);
+            __syncthreads();
+            for (int i = threadIdx.x; i < held; i += kJoinThreads) {
+                const float2 v = lm(i0 + i);
+                const float f = ex2(v.y - ref);
+                weight[i] = f;
+                l = fmaf(f, v.x, l);
+            }
+            __syncthreads();
+            if (in) {
+                const float* rows_p = a.parts + page0 * dv + col;
+                const float* rows_c = a.cparts + core0 * dv + col;
+                const int64_t step = (int64_t)a.rows * dv;
+#pragma unroll 4
+                for (int i = sg; i < held; i += groups) {
+                    const int j = i0 + i;
+                    const float4 v = *reinterpret_cast<const float4*>(j < n_pages ? rows_p + j * step
+                                                                                  : rows_c + (j - n_pages) * step);
+                    const float f = weight[i];
+                    o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
                 }
+            }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (k * 128 + lane * 4 < dv)
-                *reinterpret_cast<float4*>(&sums[warp][k * 128 + lane * 4]) = make_float4(o[k][0], o[k][1], o[k][2], o[k][3]);
+        for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
         __syncthreads();
+        if (lane == 0) red[warp] = l;
+        sums[threadIdx.x] = o;
+        __syncthreads();
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) l += red[w];
+        for (int half = groups; half > 1;) {   // the groups' sums, in a fixed tree
+            const int low = (half + 1) / 2;
+            if (sg < low && sg + low < half) {
+                const float4 v = sums[threadIdx.x + low * quads];
+                float4& t = sums[threadIdx.x];
+                t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+            }
+            half = low;
+            __syncthreads();
+        }
         const int64_t row = (int64_t)b * s.hq + hq0;
         const bool empty = nothing(m, l);
-        for (int c = threadIdx.x; c < dv; c += kJoinThreads) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) v += sums[w][c];
-            a.out[row * dv + c] = empty ? 0.f : v / l;
-        }
-        if (threadIdx.x == 0 && a.lse) a.lse[row] = log_sum(m, l);
+        if (threadIdx.x < cols && col0 + threadIdx.x < dv)
+            a.out[row * dv + col0 + threadIdx.x] = empty ? 0.f : reinterpret_cast<const float*>(sums)[threadIdx.x] / l;
+        if (threadIdx.x == 0 && col0 == 0 && a.lse) a.lse[row] = log_sum(m, l);
         return;
     }
     float acc[kScoreKeys / kJoinThreads];
@@ -1025,10 +1086,19 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttendAr
         __syncthreads();
         for (int r = warp; r < rows; r += kJoinWarps) {
             find_sets(hq0 + r0 + r);
-            float m, l;
-            total(m, l);
+            float m = -CUDART_INF_F, l = 0.f;
+            for (int i = lane; i < n; i += 32) m = fmaxf(m, lm(i).y);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float ref = m == -CUDART_INF_F ? 0.f : m;
+            for (int i = lane; i < n; i += 32) {
+                const float2 v = lm(i);
+                l = fmaf(ex2(v.y - ref), v.x, l);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             if (lane == 0) {
-                refs[r][0] = m == -CUDART_INF_F ? 0.f : m;
+                refs[r][0] = ref;
                 refs[r][1] = nothing(m, l) ? 0.f : 1.f / l;   // no weight anywhere: 0 for every key
             }
         }
@@ -1091,40 +1161,37 @@ wc_status resident_blocks(const void* kern, int threads, int smem, int* out) {
     return WC_OK;
 }
 
-// Launches one of the page kernels (its grid: as many blocks as the GPU holds
-// at once, or one per step where there are fewer) and the join.
-wc_status run(AttendArgs a, void (*kern)(const AttendArgs), int warps, int smem, int tile, cudaStream_t st) {
-    int room = 0;
-    if (resident_blocks(reinterpret_cast<const void*>(kern), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
+using Kernel = void (*)(AttendArgs);
+
+// Launches the coreset's kernel where there is one, the pages' (as many blocks
+// as the GPU holds at once, or one per tile where there are fewer), and the join.
+wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel core, int core_smem, cudaStream_t st) {
+    int room = 0, core_room = 0;
+    if (resident_blocks(reinterpret_cast<const void*>(pages), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
     const int64_t units = (int64_t)a.s.B * a.s.hkv * a.row_tiles, most = units * ((a.s.cap + tile - 1) / tile);
-    if (most > INT32_MAX) return WC_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
-    a.blocks = (int)min((most + warps - 1) / warps, (int64_t)min(room, kMaxWorkers / warps));
-    a.workers = a.blocks * warps;
-    const int64_t grid = a.blocks + a.csplits * units;
-    if (grid > INT32_MAX) return WC_ERR_UNSUPPORTED;
-    kern<<<(unsigned)grid, warps * 32, smem, st>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return WC_ERR_CUDA;
-    const int64_t chunks = (a.s.cap + kScoreKeys - 1) / kScoreKeys;
-    const int64_t join = (int64_t)a.s.B * a.s.hq + (a.scores ? chunks * a.s.B * a.s.hkv : 0);
-    if (join > INT32_MAX) return WC_ERR_UNSUPPORTED;
-    // the join's blocks may start while the last page blocks run; they wait before they read partial rows
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)join);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel, a, tile) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
+    const int64_t chunks = (a.s.cap + kScoreKeys - 1) / kScoreKeys, rows = (int64_t)a.s.B * a.s.hq;
+    // a block for 32 columns of a row while that is what fills the GPU, else for all of the row's
+    int cols = 32;
+    while (cols < a.s.dv && rows * ((a.s.dv + cols - 1) / cols) > 4 * 148) cols *= 2;
+    const int64_t join = rows * ((a.s.dv + cols - 1) / cols) + (a.scores ? chunks * a.s.B * a.s.hkv : 0);
+    if (most > INT32_MAX || join > INT32_MAX) return WC_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
+    if (a.csplits) {
+        if (units * a.csplits > INT32_MAX) return WC_ERR_UNSUPPORTED;
+        if (resident_blocks(reinterpret_cast<const void*>(core), kCoresetWarps * 32, core_smem, &core_room) != WC_OK ||
+            !launch(core, units * a.csplits, kCoresetWarps * 32, core_smem, st, a))
+            return WC_ERR_CUDA;
+    }
+    a.blocks = (int)min((most + warps - 1) / warps, (int64_t)min(room, max_warps(a.s) / warps));
+    if (!launch(pages, a.blocks, warps * 32, smem, st, a) ||
+        !launch(cache_join_kernel, join, kJoinThreads, 0, st, a, tile, a.blocks * warps, cols))
+        return WC_ERR_CUDA;
+    return WC_OK;
 }
 
 template <int DP, int RG>
 wc_status run_simt(const AttendArgs& a, cudaStream_t st) {
-    int smem = SimtSmem<DP, RG>::total;
-    if (a.csplits) smem = max(smem, CoresetSmem<8, RG, kSimtWarps>(a.s.d, a.s.dv, 4).total);
-    return run(a, cache_attend_simt_kernel<DP, RG>, kSimtWarps, smem, kSimtKeys, st);
+    return run(a, cache_attend_simt_kernel<DP, RG>, kSimtWarps, SimtSmem<DP, RG>::total, kSimtKeys,
+               cache_coreset_kernel<float, RG, 8, DP / 32>, CoresetSmem<8, RG, kCoresetWarps>(a.s.d, a.s.dv, 4).total, st);
 }
 
 template <int DP>
@@ -1140,9 +1207,10 @@ wc_status by_rows(const AttendArgs& a, cudaStream_t st) {
 template <int DP, int SETS>
 wc_status run_mma(const AttendArgs& a, cudaStream_t st) {
     constexpr int rows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
-    int smem = kMmaWarps<DP> * MmaRing<DP>::kBytes;
-    if (a.csplits) smem = max(smem, CoresetSmem<kCoresetKeys<DP>, rows, kMmaWarps<DP>>(a.s.d, a.s.dv, 2).total);
-    return run(a, cache_attend_mma_kernel<DP, SETS>, kMmaWarps<DP>, smem, kMmaKeys, st);
+    constexpr int keys = DP > 128 ? 8 : 16;   // (two stages of 16 of the widest rows leave too little room)
+    return run(a, cache_attend_mma_kernel<DP, SETS>, kMmaWarps<DP>, kMmaWarps<DP> * MmaRing<DP>::kBytes, kMmaKeys,
+               cache_coreset_kernel<__nv_bfloat16, rows, keys, DP / 32>,
+               CoresetSmem<keys, rows, kCoresetWarps>(a.s.d, a.s.dv, 2).total, st);
 }
 
 template <int DP>

@@ -28,16 +28,19 @@ struct Layout {
     size_t status;    // int32 first device error
     size_t marks;     // int32[n_pages]  references to each page (evict)
     size_t lens;      // int32[2][B]     lengths before and after (evict)
-    size_t parts;     // float[units + workers][rows][dv]  partial rows (attend)
-    size_t parts_lm;  // float2[units + workers][rows]     their normalisers and references
+    size_t parts;     // float[units + warps][rows][dv]  partial rows (attend)
+    size_t parts_lm;  // float2[units + warps][rows]     their normalisers and references
     size_t cparts;    // float[units][coreset splits][rows][dv]
     size_t cparts_lm; // float2[units][coreset splits][rows]
     size_t logits;    // float[B][hq][cap]  logits in log2 units (attend with accumulation)
     size_t end;
 };
 
-// Workers (warps) of one attention launch over the pages, at most (the partial rows are sized for them).
-constexpr int kMaxWorkers = 148 * 12;
+// Warps of one attention launch over the pages, at most: what an SM holds of the kernel for that type and width.
+inline int max_warps(const View& s) {
+    const int w = s.d > s.dv ? s.d : s.dv;
+    return 148 * (s.dtype == WC_BF16 ? (w <= 64 ? 16 : w <= 128 ? 8 : 6) : 12);
+}
 constexpr int kCoresetBlocks = 148 * 2;   // and over the coresets, beside one a unit
 
 int rows_of(const View& s);   // query rows of one unit of the attention's work
@@ -57,12 +60,29 @@ struct AttendArgs {
     int* status;
     int rows, row_tiles;   // query rows of one unit of work; units per (sequence, kv head)
     int csplits, csplit_len;
-    int blocks;            // blocks for the pages' tiles; those behind them take the coreset
-    int workers;           // their warps
+    int blocks;            // of the pages' kernel
     float qscale;          // beta * log2(e)
 };
 
 wc_status launch_attend(const AttendArgs& a, cudaStream_t st);
+
+// Launches a kernel that may start before the stream's kernel ahead of it has
+// ended (programmatic dependent launch): it calls grid_dependency_wait before
+// it reads or writes anything of the caller's.
+template <typename... A>
+bool launch(void (*kern)(A...), int64_t grid, int threads, int smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
 
 // ---------------------------------------------------------------- device side
 
@@ -121,34 +141,35 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Division of the batch's work.  The keys of every unit (sequence, kv head,
-// row tile of its group's queries) are cut into tiles; all T tiles stand in one
-// row, ordered by unit, and each of C <= T workers (a warp) takes one stretch
-// of T / C tiles, the first T % C of them one more.  Workers then have equal
-// work whatever the lengths are.  A unit that spans several workers leaves one
-// partial row set per worker; the set of unit u from worker c has slot u + c,
-// which no other pair has: along the row of tiles each next set has a larger
-// u, a larger c or both.
+// row tile of its group's queries) are cut into tiles, all T tiles stand in one
+// row, ordered by unit, and each warp takes one stretch of `per` tiles, so that
+// all have equal work whatever the lengths are.  A unit that spans several
+// stretches leaves one set of partial rows for each; the set of unit u from
+// stretch c has slot u + c, which no other pair has: along the row each next set
+// has a larger u, a larger c or both.
+// (The SMs do not get equal shares of the memory's rate: the slowest warp ends
+// at 1.15 times the mean.  Measured and not kept: four fifths of the work divided
+// so and the rest in short stretches that warps take from a counter; going on to
+// another stretch stalls a warp for longer than the evenness saves, 94 -> 106 us
+// for four sequences of 32768 tokens.)
+constexpr int kPlaces = 1024;      // places in the row that a block holds: every sequence's, or every n-th one's
 struct Share {
-    int per, more;    // T / C, T % C
-    __device__ __forceinline__ Share(int tiles, int workers) : per(tiles / workers), more(tiles - per * workers) {}
-    __device__ __forceinline__ int first(int c) const { return c * per + min(c, more); }
-    __device__ __forceinline__ int worker(int t) const {
-        const int big = more * (per + 1);
-        return t < big ? t / (per + 1) : more + (t - big) / per;
-    }
+    int total, per, count;   // tiles, tiles of a stretch, stretches
+    __device__ __forceinline__ Share(int tiles, int warps)
+        : total(tiles), per(max((tiles + warps - 1) / warps, 1)), count((tiles + per - 1) / per) {}
+    __device__ __forceinline__ int first(int c) const { return c * per; }
+    __device__ __forceinline__ int last(int c) const { return min(c * per + per, total); }
+    __device__ __forceinline__ int of(int t) const { return t / per; }
 };
 
-// Tiles of the batch, the workers that get some, and a sequence with the
-// tiles before it: the want_b-th, or the one that holds worker c's first tile.
-struct Place {
-    int total, workers;
-    int before, b;
-};
+// Tiles of the batch and the tiles before sequence want_b (where >= 0); where
+// pre is not null, the tiles before every step-th sequence go there.  All threads of the
+// block call it; `sh` holds an int and one per warp.  The host has seen to it
+// that the tiles of full tables stay below 2^31.
+struct Place { int total, before; };
 
-// All threads of the block call it; `sh` holds 2 ints + one per warp.  The
-// host has seen to it that the tiles of full tables stay below 2^31.
 template <int THREADS>
-__device__ Place find_place(const View& s, const int32_t* lens, int tile, int per_tile, int workers, int c, int want_b,
+__device__ Place scan_tiles(const View& s, const int32_t* lens, int tile, int per_tile, int want_b, int* pre, int step,
                             int* status, int* sh) {
     const int per = (s.B + THREADS - 1) / THREADS;
     const int b0 = threadIdx.x * per, b1 = min(b0 + per, s.B);
@@ -161,35 +182,22 @@ __device__ Place find_place(const View& s, const int32_t* lens, int tile, int pe
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) sh[2 + warp] = incl;
-    if (threadIdx.x == 0) { sh[0] = 0; sh[1] = s.B; }
+    if (lane == 31) sh[1 + warp] = incl;
     __syncthreads();
-    int base = 0, total = 0;
+    int at = incl - sum, total = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) base += sh[2 + w];
-        total += sh[2 + w];
+        if (w < warp) at += sh[1 + w];
+        total += sh[1 + w];
     }
-    incl += base;
-    Place p;
-    p.total = total;
-    p.workers = min(workers, total);
-    const int first = c < p.workers ? Share(total, p.workers).first(c) : total;
-    const bool mine = want_b >= 0 ? (want_b >= b0 && want_b < b1) : (first >= incl - sum && first < incl);
-    if (mine) {
-        int at = incl - sum, b = b0;
-        for (; b < b1; ++b) {
-            const int n = (checked_len(lens, b, s.cap, status) + tile - 1) / tile * per_tile;
-            if (want_b >= 0 ? b == want_b : first < at + n) break;
-            at += n;
+    if (pre || (want_b >= b0 && want_b < b1))
+        for (int b = b0; b < b1; ++b) {
+            if (pre && b % step == 0) pre[b / step] = at;
+            if (b == want_b) sh[0] = at;
+            at += (checked_len(lens, b, s.cap, status) + tile - 1) / tile * per_tile;
         }
-        sh[0] = at;
-        sh[1] = b;
-    }
     __syncthreads();
-    p.before = sh[0];
-    p.b = sh[1];
-    return p;
+    return Place{total, want_b >= 0 ? sh[0] : 0};
 }
 
 }  // namespace cache

@@ -476,6 +476,47 @@ def test_captured_step_serves_a_growing_cache():
     assert torch.equal(cache.scores, eager.scores) and cache.check() == 0
 
 
+def test_captured_behind_copies_and_other_streams():
+    """The step captured behind a copy, a memset and another stream's kernel:
+    what stands before it in the graph is done when it reads."""
+    case = Case(BF, 2, 8, 2, 64, 64, 16, 100, [1600, 900], seed=23)
+    cache, q, lens = make(case)
+    core = tuple(t.cuda() for t in coreset_of(case, 100, 5))
+    plain_out = cache.attend(q, lens)
+    core_out = cache.attend(q, lens, coreset=core)
+    q2, lens2, big = torch.zeros_like(q), torch.zeros_like(lens), torch.randn(1 << 24, device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q2.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big.mul_(1.0)
+            lens2.copy_(lens)
+        q2.copy_(q)
+        torch.cuda.current_stream().wait_stream(side)
+        a = cache.attend(q2, lens2)
+        q2.zero_()
+        q2.copy_(q)
+        b = cache.attend(q2, lens2, coreset=core)
+        q2.zero_()
+        lens2.zero_()
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(a, plain_out) and torch.equal(b, core_out)
+    # and eagerly, each call behind the one before
+    for _ in range(20):
+        big.mul_(1.0)
+        lens2.copy_(lens)
+        q2.copy_(q)
+        a = cache.attend(q2, lens2)
+        b = cache.attend(q2, lens2, coreset=core)
+        c = cache.attend(q2, lens2)
+        lens2.zero_()
+        q2.zero_()
+        assert torch.equal(a, plain_out) and torch.equal(b, core_out) and torch.equal(c, plain_out)
+
+
 def test_other_stream():
     case = Case(BF, 4, 8, 2, 64, 64, 16, 100, [1600, 900, 0, 5], seed=21)
     cache, q, lens = make(case)
