@@ -640,7 +640,7 @@ wc_status wc_cache_attend(const wc_cache* cache, const void* Q, int64_t q_batch,
     AttendArgs a{};
     wc_status e = make_view(cache, &a.s);
     if (e != WC_OK) return e;
-    if (r < 0 || r > 4096 || (r > 0 && (!Ks || !W || !aligned(Ks, 16) || !aligned(W, 4) || !aligned(rank, 4))))
+    if (r < 0 || r > 4096 || (r > 0 && (!Ks || !W || !aligned(Ks, 16) || !aligned(W, 16) || !aligned(rank, 4))))
         return WC_ERR_INVALID;
     if (!Q || !k || !v || !table || !lens || !out || !aligned(Q, a.s.esize) || !aligned(k, 16) || !aligned(v, 16) ||
         !aligned(table, 4) || !aligned(lens, 4) || !aligned(out, 4) || !aligned(lse, 4) || !aligned(scores, 4))

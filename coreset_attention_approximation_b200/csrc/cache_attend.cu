@@ -287,8 +287,8 @@ __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int g0,
 }
 
 // Shared memory of one coreset block, in bytes: two stages a warp of NT keys
-// and their rows of W (as they lie in memory, dv + 1 values each).  The warps'
-// sums go where the stages were.
+// and their rows of W (as they lie in memory, dv + 1 values each, and up to 12
+// bytes before them).  The warps' sums go where the stages were.
 template <int NT, int RG, int WARPS>
 struct CoresetSmem {
     int k_row, w_row, w, stage, q, p, total;
@@ -297,7 +297,7 @@ struct CoresetSmem {
         if ((k_row / 16) % 2 == 0) k_row += 16;
         w_row = (dv + 1) * 4;
         w = NT * k_row;
-        stage = (w + NT * w_row + 15) / 16 * 16;
+        stage = (w + 12 + NT * w_row + 15) / 16 * 16;
         const int stages = WARPS * 2 * stage, merge = WARPS * RG * (dv + 2) * 4;
         q = ((stages > merge ? stages : merge) + 15) / 16 * 16;
         p = q + RG * d * 4;
@@ -311,11 +311,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 
 // One block of the coreset's share: rows [first, last) of unit (b, h)'s
 // coreset against RG query rows, NT at a time for each warp.  W is fp32 with
-// rows of dv + 1 values (no 16-byte alignment), so a step's rows, which lie
-// side by side, come in by 4-byte asynchronous copies while the step before is
-// summed; a lane holds columns lane, lane + 32, ... and the row's last value is
-// its weight in the normaliser.  Sums in fp32 on CUDA cores: W's values cancel
-// one another, and there are few rows.
+// rows of dv + 1 values, which have no 16-byte alignment; a step's rows lie side
+// by side, so the 16-byte pieces that hold them are copied (4-byte copies took
+// 1.3 times as long over all), the last few values one by one.  A lane holds
+// columns lane, lane + 32, ... and the row's last value is its weight in the
+// normaliser.  Sums in fp32 on CUDA cores: W's values cancel one another.
 constexpr int kCoresetWarps = 4;
 
 template <typename T, int RG, int NT, int COLS>
@@ -352,8 +352,10 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
                 if (row < live) cp_async16(kd + row * L.k_row + c * 16, k + i * 16);
                 for (c += 32; c >= ck; c -= ck) ++row;
             }
-            const float* w = a.W + (base + at) * (s.dv + 1);
-            for (int i = lane; i < live * (s.dv + 1); i += 32) cp_async4(wd + i * 4, w + i);
+            const int64_t w0 = (base + at) * (s.dv + 1), w1 = w0 + live * (s.dv + 1);   // values [w0, w1) of W
+            const int pieces = (int)(w1 / 4 - w0 / 4);
+            for (int i = lane; i < pieces; i += 32) cp_async16(wd + i * 16, a.W + (w0 / 4 + i) * 4);
+            if (lane < (int)(w1 & 3)) cp_async4(wd + pieces * 16 + lane * 4, a.W + (w1 / 4) * 4 + lane);
         }
         cp_async_commit();
     };
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
         cp_async_wait<1>();
         __syncwarp();
         const char* krows = stages + stage * L.stage;
-        const float* wrows = reinterpret_cast<const float*>(krows + L.w);
+        const float* wrows = reinterpret_cast<const float*>(krows + L.w) + (int)(((base + at) * (s.dv + 1)) & 3);
         float x[RG];
         tile_logits<T, RG, NT>(krows, L.k_row, q, s.d, x);
         const int key = lane % NT, live = min(NT, last - at);
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
             if (lane < NT) p[key * RG + g] = w;
         }
         __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; j < live; ++j) {
             const float* w = wrows + j * (s.dv + 1);
             float y[COLS], e[RG];
@@ -403,7 +405,15 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
             for (int i = 0; i < COLS; ++i) y[i] = lane + 32 * i < s.dv ? w[lane + 32 * i] : 0.f;
             const float z = w[s.dv];
 #pragma unroll
-            for (int g = 0; g < RG; ++g) e[g] = p[j * RG + g];
+            for (int g = 0; g < RG; g += 4) {
+                if (RG % 4 == 0) {
+                    const float4 v = *reinterpret_cast<const float4*>(p + j * RG + g);
+                    e[g] = v.x, e[(g + 1) % RG] = v.y, e[(g + 2) % RG] = v.z, e[(g + 3) % RG] = v.w;
+                } else {
+#pragma unroll
+                    for (int k = g; k < RG; ++k) e[k] = p[j * RG + k];
+                }
+            }
 #pragma unroll
             for (int g = 0; g < RG; ++g) {
                 l[g] = fmaf(e[g], z, l[g]);
@@ -1207,7 +1217,7 @@ wc_status by_rows(const AttendArgs& a, cudaStream_t st) {
 template <int DP, int SETS>
 wc_status run_mma(const AttendArgs& a, cudaStream_t st) {
     constexpr int rows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
-    constexpr int keys = DP > 128 ? 8 : 16;   // (two stages of 16 of the widest rows leave too little room)
+    constexpr int keys = 8;   // (with 16, half as many warps an SM: 1.2 times as long)
     return run(a, cache_attend_mma_kernel<DP, SETS>, kMmaWarps<DP>, kMmaWarps<DP> * MmaRing<DP>::kBytes, kMmaKeys,
                cache_coreset_kernel<__nv_bfloat16, rows, keys, DP / 32>,
                CoresetSmem<keys, rows, kCoresetWarps>(a.s.d, a.s.dv, 2).total, st);

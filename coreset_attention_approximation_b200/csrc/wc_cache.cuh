@@ -41,7 +41,7 @@ inline int max_warps(const View& s) {
     const int w = s.d > s.dv ? s.d : s.dv;
     return 148 * (s.dtype == WC_BF16 ? (w <= 64 ? 16 : w <= 128 ? 8 : 6) : 12);
 }
-constexpr int kCoresetBlocks = 148 * 2;   // and over the coresets, beside one a unit
+constexpr int kCoresetBlocks = 148 * 4;   // and over the coresets, beside one a unit
 
 int rows_of(const View& s);   // query rows of one unit of the attention's work
 wc_status make_view(const wc_cache* in, View* o);
