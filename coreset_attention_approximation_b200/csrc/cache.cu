@@ -91,7 +91,7 @@ Layout make_layout(const View& s, bool accumulate) {
     const int rows = rows_of(s), tiles = (s.group + rows - 1) / rows;
     const size_t units = (size_t)s.B * s.hkv * tiles, set = sizeof(float) * rows * s.dv, lm = sizeof(float2) * rows;
     L.status = take(256);
-    L.marks = take(sizeof(int32_t) * (size_t)s.n_pages);
+    L.marks = take(sizeof(int32_t) * 2 * (size_t)s.n_pages);
     L.lens = take(sizeof(int32_t) * 2 * (size_t)s.B);
     L.parts = take((units + max_warps(s)) * set);
     L.parts_lm = take((units + max_warps(s)) * lm);
@@ -213,7 +213,9 @@ struct EvictArgs {
     const int32_t* lens; const float* scores;
     float* scores_into;       // may be scores
     int32_t* idx; int32_t* lens_out;
-    int32_t* marks; int32_t* ws_lens;
+    int32_t* marks;           // int32[2][n_pages], see mark_pages
+    int32_t* phase;           // which half this call uses; and a copy for the move
+    int32_t* ws_lens;
     int* status;
 };
 
@@ -231,14 +233,17 @@ constexpr int kSelectSlice = 4096;            // positions of a block before ano
 constexpr int kSelectHeld = 40960;            // keys a block holds in shared memory, at most
 
 // References to the pages of sequence b: one for each page its tokens use, one
-// for each page of `into` that it will write.
-__device__ __forceinline__ void mark_pages(const EvictArgs& a, int b, int len, int kept, int first, int step) {
+// for each page of `into` that it will write.  The counts start at 0: of two
+// halves the calls use one after the other, and each call clears the half that
+// the next will use (its last readers are done), which spares a launch.
+__device__ __forceinline__ void mark_pages(const EvictArgs& a, int32_t* marks, int b, int len, int kept, int first,
+                                           int step) {
     const View& s = a.s;
     const int used = (len + s.page - 1) / s.page, written = a.into ? (kept + s.page - 1) / s.page : 0;
     for (int i = first; i < used + written; i += step) {
         const int32_t* row = (i < used ? s.table : a.into) + (int64_t)b * s.max_pages;
         const int p = row[i < used ? i : i - used];
-        if ((unsigned)p < (unsigned)s.n_pages) atomicAdd(a.marks + p, 1);
+        if ((unsigned)p < (unsigned)s.n_pages) atomicAdd(marks + p, 1);
     }
 }
 
@@ -280,6 +285,7 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Evic
     __shared__ int block_counts[2];
     __shared__ uint32_t s_bin;
     __shared__ int s_left;
+    grid_dependency_wait();
     grid_dependents_launch();
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
@@ -288,8 +294,13 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Evic
     const int unit = blockIdx.x / ranks, h = unit % s.hkv, b = unit / s.hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = checked_len(a.lens, b, s.cap, a.status), kept = min(len, a.keep);
+    const int half = *a.phase & 1;
+    for (int64_t i = (int64_t)blockIdx.x * kSelectThreads + tid; i < s.n_pages; i += (int64_t)gridDim.x * kSelectThreads)
+        a.marks[(int64_t)(half ^ 1) * s.n_pages + i] = 0;
+    if (blockIdx.x == 0 && tid == 0) a.phase[1] = half;
     if (h == 0) {
-        mark_pages(a, b, len, kept, rank * kSelectThreads + tid, ranks * kSelectThreads);
+        mark_pages(a, a.marks + (int64_t)half * s.n_pages, b, len, kept, rank * kSelectThreads + tid,
+                   ranks * kSelectThreads);
         if (rank == 0 && tid == 0) {
             a.ws_lens[2 * b] = len;
             a.ws_lens[2 * b + 1] = kept;
@@ -406,23 +417,25 @@ constexpr int kMoveSlice = 64;          // in place: bytes of a row that one blo
 // outside the pool, or a page to be written that is named more than once.
 __device__ bool refused(const EvictArgs& a, int b, int len, int kept) {
     const View& s = a.s;
+    const int32_t* marks = a.marks + (int64_t)a.phase[1] * s.n_pages;
     const int used = (len + s.page - 1) / s.page, written = (kept + s.page - 1) / s.page;
     int bad = 0;
     const bool moves = a.into || len > kept;
     for (int i = threadIdx.x; i < used; i += blockDim.x) {
         const int p = s.table[(int64_t)b * s.max_pages + i];
         if ((unsigned)p >= (unsigned)s.n_pages) bad |= 1;
-        else if (!a.into && moves && i < written && a.marks[p] != 1) bad |= 2;
+        else if (!a.into && moves && i < written && marks[p] != 1) bad |= 2;
     }
     if (a.into)
         for (int i = threadIdx.x; i < written; i += blockDim.x) {
             const int p = a.into[(int64_t)b * s.max_pages + i];
             if ((unsigned)p >= (unsigned)s.n_pages) bad |= 1;
-            else if (a.marks[p] != 1) bad |= 2;
+            else if (marks[p] != 1) bad |= 2;
         }
-    const int any1 = __syncthreads_or(bad & 1), any2 = __syncthreads_or(bad & 2);
-    if ((any1 || any2) && threadIdx.x == 0) record_status(a.status, any1 ? WC_ERR_BOUNDS : WC_ERR_INVALID);
-    return any1 || any2;
+    if (!__syncthreads_or(bad)) return false;
+    const int outside = __syncthreads_or(bad & 1);
+    if (threadIdx.x == 0) record_status(a.status, outside ? WC_ERR_BOUNDS : WC_ERR_INVALID);
+    return true;
 }
 
 // The scores of one (sequence, kv head), a stretch read whole before it is
@@ -499,21 +512,13 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArg
     const View& s = a.s;
     const int h = blockIdx.y, b = blockIdx.z, part = blockIdx.x;
     const int len = a.ws_lens[2 * b], kept = a.ws_lens[2 * b + 1];
+    if (part == 0 && h == 0 && b == 0 && threadIdx.x == 0) a.phase[0] = a.phase[1] ^ 1;
     constexpr int kBlockRows = kMoveThreads / 32 * kCopyRows;
     if (part > 0 && (a.into ? (part - 1) * kBlockRows >= kept : len <= kept)) return;
-    const bool no = refused(a, b, len, kept);
-    if (part == 0) {
-        move_scores(a, b, h, len, kept, no, stage);
-        return;
-    }
-    if (no) return;
-    if (!a.into) {
-        move_in_place(a, b, h, part - 1, kept, stage);
-        return;
-    }
+    // where a lane's row comes from and goes to, on its way while the pages are checked
     const int lane = threadIdx.x & 31, j = (part - 1) * kBlockRows + (threadIdx.x >> 5) * kCopyRows + lane;
     RowCopy r{nullptr, nullptr, nullptr, nullptr, false};
-    if (lane < kCopyRows && j < kept) {
+    if (part > 0 && a.into && lane < kCopyRows && j < kept) {
         const int at = a.idx[((int64_t)b * s.hkv + h) * a.keep + j], tp = page_of(s, at), slot = at - tp * s.page;
         const int to = page_of(s, j), to_slot = j - to * s.page;
         const int64_t from_page = s.table[(int64_t)b * s.max_pages + tp], to_page = a.into[(int64_t)b * s.max_pages + to];
@@ -523,7 +528,11 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArg
         r.vd = a.vp + to_page * s.v_page + h * s.v_head + (int64_t)to_slot * s.v_token;
         r.ok = true;
     }
-    copy_rows(r, s.d * s.esize / 16, s.dv * s.esize / 16);
+    const bool no = refused(a, b, len, kept);
+    if (part == 0) move_scores(a, b, h, len, kept, no, stage);
+    else if (no) return;
+    else if (a.into) copy_rows(r, s.d * s.esize / 16, s.dv * s.esize / 16);
+    else move_in_place(a, b, h, part - 1, kept, stage);
 }
 
 // The two kernels' shared-memory limits, once per device.
@@ -544,7 +553,6 @@ wc_status launch_evict(const EvictArgs& a, cudaStream_t st) {
     const View& s = a.s;
     wc_status e = evict_setup();
     if (e != WC_OK) return e;
-    if (cudaMemsetAsync(a.marks, 0, sizeof(int32_t) * (size_t)s.n_pages, st) != cudaSuccess) return WC_ERR_CUDA;
     // blocks of one (sequence, kv head): one for each kSelectSlice positions, while they leave no SM without a unit
     const int64_t units = (int64_t)s.B * s.hkv;
     int ranks = 1;
@@ -552,26 +560,26 @@ wc_status launch_evict(const EvictArgs& a, cudaStream_t st) {
     if (units * ranks > INT32_MAX || s.hkv > 65535) return WC_ERR_UNSUPPORTED;
     const int per = ((s.cap + ranks - 1) / ranks + 31) / 32 * 32;
     const int held = per < kSelectHeld ? per : kSelectHeld;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = ranks;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * ranks));
     cfg.blockDim = dim3(kSelectThreads);
     cfg.dynamicSmemBytes = (size_t)held * 4;
     cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, cache_select_kernel, a, held) != cudaSuccess) return WC_ERR_CUDA;
     const int slices = (s.d * s.esize + kMoveSlice - 1) / kMoveSlice + (s.dv * s.esize + kMoveSlice - 1) / kMoveSlice;
     const int rows = kMoveThreads / 32 * kCopyRows;
-    at = cudaLaunchAttribute{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(1 + (a.into ? (a.keep + rows - 1) / rows : slices), s.hkv, s.B);
     cfg.blockDim = dim3(kMoveThreads);
     cfg.dynamicSmemBytes = kMoveBytes;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, cache_move_kernel, a) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
 }
 
@@ -695,6 +703,7 @@ wc_status wc_cache_evict(const wc_cache* cache, int32_t keep, int32_t sink, int3
     a.scores_into = scores_into ? scores_into : const_cast<float*>(scores);
     a.idx = idx; a.lens_out = lens_out;
     a.marks = reinterpret_cast<int32_t*>(w + L.marks);
+    a.phase = reinterpret_cast<int32_t*>(w + L.status + 64);
     a.ws_lens = reinterpret_cast<int32_t*>(w + L.lens);
     a.status = static_cast<int*>(ws);
     return launch_evict(a, static_cast<cudaStream_t>(stream));

@@ -25,8 +25,8 @@ struct View {
 
 // Workspace of the cache calls (256-byte aligned regions).
 struct Layout {
-    size_t status;    // int32 first device error
-    size_t marks;     // int32[n_pages]  references to each page (evict)
+    size_t status;    // int32 first device error; 64 bytes on, int32[2]: the half of `marks` in use (evict)
+    size_t marks;     // int32[2][n_pages]  references to each page (evict)
     size_t lens;      // int32[2][B]     lengths before and after (evict)
     size_t parts;     // float[units + warps][rows][dv]  partial rows (attend)
     size_t parts_lm;  // float2[units + warps][rows]     their normalisers and references

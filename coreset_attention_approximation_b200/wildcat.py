@@ -359,7 +359,8 @@ class HostPipeline:
 
 def _strides(t):
     """Strides of a 4-axis tensor's first three axes, 0 where the axis has one entry."""
-    return [st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3])]
+    (a, b, c, _), (x, y, z, _) = t.shape, t.stride()
+    return x if a > 1 else 0, y if b > 1 else 0, z if c > 1 else 0
 
 
 class PagedCache:
@@ -417,11 +418,16 @@ class PagedCache:
         if self.device.type != "cuda":
             raise WildcatError(1, "PagedCache: the pages are on a GPU")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-        # what every call passes on, looked up once (a decode step's calls are as short as their checks)
+        # what every call passes on, looked up once (a decode step's kernels are as short as the calls that launch them)
         self._shape_ref = ctypes.byref(self.shape)
+        self._pools = (k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr())
         self._p_scores = None if scores is None else scores.data_ptr()
+        self._room = (self.ws.data_ptr(), n)
         self._q_shape, self._o_shape = (self.batch, self.hq, self.d), (self.batch, self.hq, self.dv)
+        self._seqs, self._index = (self.batch,), self.device.index
         self._kept = (self.k_pages, self.v_pages, self.table, self.scores, self.ws)
+        L = lib()
+        self._append, self._attend, self._evict = L.wc_cache_append, L.wc_cache_attend, L.wc_cache_evict
 
     # ---- arguments
 
@@ -453,19 +459,19 @@ class PagedCache:
         """call(*args, stream) on the given stream, or the device's current
         one, with the pages' device current.  The caching allocator is told of
         the tensors' use on a given stream."""
-        s = torch.cuda.current_stream(self.device)
-        if stream is not None and stream != s:
+        handle = torch._C._cuda_getCurrentRawStream(self._index)
+        if stream is not None and stream.cuda_stream != handle:
             if stream.device != self.device:
                 raise WildcatError(1, f"{what}: the stream is another device's")
             for t in tensors + self._kept:
                 if t is not None:
                     t.record_stream(stream)
-            s = stream
-        if torch.cuda.current_device() == self.device.index:
-            code = call(*args, s.cuda_stream)
+            handle = stream.cuda_stream
+        if torch.cuda.current_device() == self._index:
+            code = call(*args, handle)
         else:
             with torch.cuda.device(self.device):
-                code = call(*args, s.cuda_stream)
+                code = call(*args, handle)
         if code != 0:
             raise WildcatError(code, what)
 
@@ -487,15 +493,14 @@ class PagedCache:
         t = K.shape[2] if K.dim() == 4 else -1
         self._rows(K, "K", (self.batch, self.hkv, t, self.d))
         self._rows(V, "V", (self.batch, self.hkv, t, self.dv))
-        self._tensor(pos, "pos", (self.batch,), torch.int32)
+        self._tensor(pos, "pos", self._seqs, torch.int32)
         if count is not None:
-            self._tensor(count, "count", (self.batch,), torch.int32)
+            self._tensor(count, "count", self._seqs, torch.int32)
         ks, vs = WcRowStrides(*_strides(K)), WcRowStrides(*_strides(V))
-        self._launch(lib().wc_cache_append, "wc_cache_append", stream,
-                     (self._shape_ref, t, K.data_ptr(), ctypes.byref(ks), V.data_ptr(), ctypes.byref(vs),
-                      pos.data_ptr(), None if count is None else count.data_ptr(), self.k_pages.data_ptr(),
-                      self.v_pages.data_ptr(), self.table.data_ptr(), self._p_scores, self.ws.data_ptr(),
-                      self.ws.numel()), (K, V, pos, count))
+        self._launch(self._append, "wc_cache_append", stream,
+                     (self._shape_ref, t, K.data_ptr(), ks, V.data_ptr(), vs, pos.data_ptr(),
+                      None if count is None else count.data_ptr(), *self._pools, self._p_scores, *self._room),
+                     (K, V, pos, count))
 
     def attend(self, Q, lens, *, coreset=None, accumulate=False, return_lse=False, out=None, stream=None):
         """Attention of one new token per sequence: Q [B, Hq, d] over the first
@@ -504,7 +509,7 @@ class PagedCache:
         Returns out [B, Hq, dv] fp32, or (out, lse [B, Hq]).  accumulate: adds
         each key's attention weight, summed over its queries, to `scores`."""
         self._rows(Q, "Q", self._q_shape)
-        self._tensor(lens, "lens", (self.batch,), torch.int32)
+        self._tensor(lens, "lens", self._seqs, torch.int32)
         if accumulate and self.scores is None:
             raise WildcatError(1, "PagedCache.attend: accumulate needs scores")
         Ks = W = rank = None
@@ -522,12 +527,12 @@ class PagedCache:
             self._tensor(out, "out", self._o_shape, torch.float32)
         lse = self._empty((self.batch, self.hq), torch.float32, stream) if return_lse else None
         sq = Q.stride()
-        self._launch(lib().wc_cache_attend, "wc_cache_attend", stream,
-                     (self._shape_ref, Q.data_ptr(), sq[0], sq[1], self.k_pages.data_ptr(), self.v_pages.data_ptr(),
-                      self.table.data_ptr(), lens.data_ptr(), r, None if r == 0 else Ks.data_ptr(),
-                      None if r == 0 else W.data_ptr(), None if rank is None else rank.data_ptr(), out.data_ptr(),
-                      None if lse is None else lse.data_ptr(), self._p_scores if accumulate else None,
-                      self.ws.data_ptr(), self.ws.numel()), (Q, lens, Ks, W, rank, out, lse))
+        self._launch(self._attend, "wc_cache_attend", stream,
+                     (self._shape_ref, Q.data_ptr(), sq[0], sq[1], *self._pools, lens.data_ptr(), r,
+                      None if r == 0 else Ks.data_ptr(), None if r == 0 else W.data_ptr(),
+                      None if rank is None else rank.data_ptr(), out.data_ptr(),
+                      None if lse is None else lse.data_ptr(), self._p_scores if accumulate else None, *self._room),
+                     (Q, lens, Ks, W, rank, out, lse))
         return (out, lse) if return_lse else out
 
     def evict(self, lens, keep, *, sink=0, recent=0, into=None, scores_into=None, lens_out=None, stream=None):
@@ -541,7 +546,7 @@ class PagedCache:
         (lens_out may be lens itself).  A sequence that cannot be moved (a page
         outside the pool, a page to be written that is named twice) stays as it
         is; `check()` reports it."""
-        self._tensor(lens, "lens", (self.batch,), torch.int32)
+        self._tensor(lens, "lens", self._seqs, torch.int32)
         if self.scores is None:
             raise WildcatError(1, "PagedCache.evict: needs scores")
         if into is not None:
@@ -553,15 +558,13 @@ class PagedCache:
             raise WildcatError(1, "PagedCache.evict: 1 <= keep <= capacity, sink + recent <= keep")
         idx = self._empty((self.batch, self.hkv, keep), torch.int32, stream)
         if lens_out is None:
-            lens_out = self._empty((self.batch,), torch.int32, stream)
+            lens_out = self._empty(self._seqs, torch.int32, stream)
         else:
-            self._tensor(lens_out, "lens_out", (self.batch,), torch.int32)
-        self._launch(lib().wc_cache_evict, "wc_cache_evict", stream,
-                     (self._shape_ref, keep, sink, recent, self.k_pages.data_ptr(), self.v_pages.data_ptr(),
-                      self.table.data_ptr(), None if into is None else into.data_ptr(), lens.data_ptr(),
-                      self._p_scores, None if scores_into is None else scores_into.data_ptr(), idx.data_ptr(),
-                      lens_out.data_ptr(), self.ws.data_ptr(), self.ws.numel()),
-                     (lens, into, scores_into, idx, lens_out))
+            self._tensor(lens_out, "lens_out", self._seqs, torch.int32)
+        self._launch(self._evict, "wc_cache_evict", stream,
+                     (self._shape_ref, keep, sink, recent, *self._pools, None if into is None else into.data_ptr(),
+                      lens.data_ptr(), self._p_scores, None if scores_into is None else scores_into.data_ptr(),
+                      idx.data_ptr(), lens_out.data_ptr(), *self._room), (lens, into, scores_into, idx, lens_out))
         return dict(idx=idx, lens=lens_out)
 
     def check(self, stream=None) -> int:
