@@ -226,7 +226,8 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
+constexpr int kSelectBins = 2048 / kSelectThreads;   // of a thread
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectCluster = 8;             // blocks that may share one (sequence, kv head)
 constexpr int kSelectSlice = 4096;            // positions of a block before another one joins it
@@ -257,9 +258,9 @@ __device__ __forceinline__ int block_scan(int v, int* sh) {
     }
     if (lane == 31) sh[warp] = v;
     __syncthreads();
-    int w = sh[lane];
+    int w = lane < kSelectWarps ? sh[lane] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < kSelectWarps; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += u;
     }
@@ -277,12 +278,12 @@ __device__ __forceinline__ int block_scan(int v, int* sh) {
 // keys are read from memory once and held in shared memory where they fit.
 // Bound by the latency of the passes (a few barriers each) for the lengths of
 // real caches.
-__global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const EvictArgs a, int held) {
+__global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_select_kernel(const EvictArgs a, int held) {
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ __align__(16) int hist[3][2048];   // (read two at a time)
+    __shared__ __align__(16) int hist[3][2048];   // (read four at a time)
     __shared__ int sh[kSelectWarps];
-    __shared__ int counts[kSelectWarps][2];
-    __shared__ int block_counts[2];
+    __shared__ int2 counts[kSelectWarps];
+    __shared__ int2 block_counts;
     __shared__ uint32_t s_bin;
     __shared__ int s_left;
     grid_dependency_wait();
@@ -321,6 +322,7 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Evic
     for (int i = tid; i < 3 * 2048; i += kSelectThreads) (&hist[0][0])[i] = 0;
     auto key = [&](int i) { return hold ? keys[i - lo] : score_key(x[i]); };
     if (hold)
+#pragma unroll 4
         for (int i = lo + tid; i < hi; i += kSelectThreads) keys[i - lo] = score_key(x[i]);
     uint32_t prefix = 0, mask = 0;
     int left = want;
@@ -335,20 +337,40 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Evic
                 if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shifts[pass]) & (bins - 1)], 1);
             }
             cluster.sync();
-            // from the top bin down: the bin in which the `left`-th key lies
-            const int up = bins - 1 - 2 * tid;
-            int n1 = 0, n0 = 0;
-            if (up >= 1)
-                for (int r = 0; r < ranks; ++r) {
-                    const int2 v = *reinterpret_cast<const int2*>(cluster.map_shared_rank(&hist[pass][up - 1], r));
-                    n0 += v.x;
-                    n1 += v.y;
+            // from the top bin down: the bin in which the `left`-th key lies; a thread has kSelectBins of
+            // them, from bin `low` up, and takes every block's counts, all loads in flight
+            const int low = bins - kSelectBins * (tid + 1);
+            int n[kSelectBins], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kSelectBins; ++i) n[i] = 0;
+            if (low >= 0) {
+#pragma unroll
+                for (int i = 0; i < kSelectBins; i += 4) {
+                    int4 v[kSelectCluster];
+#pragma unroll
+                    for (int r = 0; r < kSelectCluster; ++r)
+                        v[r] = r < ranks ? *reinterpret_cast<const int4*>(
+                                               cluster.map_shared_rank(&hist[pass][low + i], r))
+                                         : make_int4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < kSelectCluster; ++r) {
+                        n[i] += v[r].x, n[i + 1] += v[r].y, n[i + 2] += v[r].z, n[i + 3] += v[r].w;
+                    }
                 }
-            const int incl = block_scan(n1 + n0, sh), before = incl - n1 - n0;
+            }
+#pragma unroll
+            for (int i = 0; i < kSelectBins; ++i) sum += n[i];
+            const int incl = block_scan(sum, sh);
+            int before = incl - sum;
             if (before < left && left <= incl) {
-                const bool top = left <= before + n1;
-                s_bin = top ? up : up - 1;
-                s_left = left - before - (top ? 0 : n1);
+#pragma unroll
+                for (int i = kSelectBins - 1; i >= 0; --i) {
+                    if (before < left && left <= before + n[i]) {
+                        s_bin = low + i;
+                        s_left = left - before;
+                    }
+                    before += n[i];
+                }
             }
             __syncthreads();
             prefix |= s_bin << shifts[pass];
@@ -376,25 +398,27 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Evic
         n_above += __popc(__ballot_sync(0xffffffffu, above));
         n_tie += __popc(__ballot_sync(0xffffffffu, tie));
     }
-    if (lane == 0) counts[warp][0] = n_above, counts[warp][1] = n_tie;
+    if (lane == 0) counts[warp] = make_int2(n_above, n_tie);
     __syncthreads();
-    if (warp == 0) {
-        int u = counts[lane][0], v = counts[lane][1];
+    if (warp == 0) {   // the counts before each warp, and the block's
+        const int2 own = lane < kSelectWarps ? counts[lane] : make_int2(0, 0);
+        int2 c = own;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            u += __shfl_xor_sync(0xffffffffu, u, o);
-            v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, c.x, o), v = __shfl_up_sync(0xffffffffu, c.y, o);
+            if (lane >= o) c.x += u, c.y += v;
         }
-        if (lane == 0) block_counts[0] = u, block_counts[1] = v;
+        if (lane < kSelectWarps) counts[lane] = make_int2(c.x - own.x, c.y - own.y);
+        if (lane == 31) block_counts = c;
     }
     cluster.sync();
-    int above_before = 0, ties_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        const int* c = cluster.map_shared_rank(block_counts, r);
-        above_before += c[0];
-        ties_before += c[1];
-    }
-    for (int w = 0; w < warp; ++w) above_before += counts[w][0], ties_before += counts[w][1];
+    int2 blocks[kSelectCluster];
+#pragma unroll
+    for (int r = 0; r < kSelectCluster; ++r)
+        blocks[r] = r < rank ? *cluster.map_shared_rank(&block_counts, r) : make_int2(0, 0);
+    int above_before = counts[warp].x, ties_before = counts[warp].y;
+#pragma unroll
+    for (int r = 0; r < kSelectCluster; ++r) above_before += blocks[r].x, ties_before += blocks[r].y;
     int at = above_before + min(ties_before, left);
     for (int i = w0; i < w1; i += 32) {
         bool above, tie;
@@ -411,6 +435,7 @@ __global__ void __launch_bounds__(kSelectThreads) cache_select_kernel(const Evic
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBytes = 64 * 1024;   // in place: bytes staged at a time
+constexpr int kMoveBytesInto = 16 * 1024;   // into other pages: of scores (the rows need none, and more blocks fit)
 constexpr int kMoveSlice = 64;          // in place: bytes of a row that one block moves
 
 // Whether a sequence's move is refused, and the reason recorded: a page
@@ -453,9 +478,9 @@ __device__ void move_scores(const EvictArgs& a, int b, int h, int len, int kept,
     const float* from = a.scores + unit * s.cap;
     float* to = a.scores_into + unit * s.cap;
     float* sh = reinterpret_cast<float*>(stage);
-    constexpr int kChunk = kMoveBytes / 4;
-    for (int j0 = 0; j0 < kept; j0 += kChunk) {
-        const int n = min(kChunk, kept - j0);
+    const int chunk = (a.into ? kMoveBytesInto : kMoveBytes) / 4;
+    for (int j0 = 0; j0 < kept; j0 += chunk) {
+        const int n = min(chunk, kept - j0);
 #pragma unroll 4
         for (int j = threadIdx.x; j < n; j += kMoveThreads) sh[j] = from[idx[j0 + j]];
         __syncthreads();
@@ -578,7 +603,7 @@ wc_status launch_evict(const EvictArgs& a, cudaStream_t st) {
     const int rows = kMoveThreads / 32 * kCopyRows;
     cfg.gridDim = dim3(1 + (a.into ? (a.keep + rows - 1) / rows : slices), s.hkv, s.B);
     cfg.blockDim = dim3(kMoveThreads);
-    cfg.dynamicSmemBytes = kMoveBytes;
+    cfg.dynamicSmemBytes = a.into ? kMoveBytesInto : kMoveBytes;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, cache_move_kernel, a) == cudaSuccess ? WC_OK : WC_ERR_CUDA;
 }
