@@ -28,20 +28,48 @@ namespace {
 
 constexpr int kSimtWarps = 4;
 
-template <typename T> __device__ __forceinline__ void load_chunk(const char* p, float* x);
-template <> __device__ __forceinline__ void load_chunk<float>(const char* p, float* x) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+// Pairs of fp32 values in one 64-bit register, added and multiplied as one:
+// half the instructions where the issue of sums is what bounds a loop.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
 }
-template <> __device__ __forceinline__ void load_chunk<__nv_bfloat16>(const char* p, float* x) {
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t p;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
+    return p;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t p;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
+    return p;
+}
+// x y + z
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t p;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(x), "l"(y), "l"(z));
+    return p;
+}
+__device__ __forceinline__ float2 halves(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+
+template <typename T> __device__ __forceinline__ void load_chunk(const char* p, uint64_t* x);
+template <> __device__ __forceinline__ void load_chunk<float>(const char* p, uint64_t* x) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+}
+template <> __device__ __forceinline__ void load_chunk<__nv_bfloat16>(const char* p, uint64_t* x) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = pair_of(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
+
 // Logits of NT staged keys against RG query rows: lane = (key, part of d).
 // Every lane ends with its key's whole sums.
 template <typename T, int RG, int NT>
@@ -49,22 +77,27 @@ __device__ __forceinline__ void tile_logits(const char* krows, int k_row, const 
     constexpr int kPer = 16 / sizeof(T);
     const int lane = threadIdx.x & 31, key = lane % NT, part = lane / NT;
     const char* row = krows + key * k_row;
+    uint64_t sum[RG];
 #pragma unroll
-    for (int g = 0; g < RG; ++g) s[g] = 0.f;
+    for (int g = 0; g < RG; ++g) sum[g] = 0;
+#pragma unroll 4
     for (int c = part; c < d / kPer; c += 32 / NT) {
-        float x[kPer];
+        uint64_t x[kPer / 2];
         load_chunk<T>(row + c * 16, x);
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
 #pragma unroll
             for (int i = 0; i < kPer; i += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(q + g * d + c * kPer + i);
-                s[g] = fmaf(x[i], y.x, s[g]);
-                s[g] = fmaf(x[i + 1], y.y, s[g]);
-                s[g] = fmaf(x[i + 2], y.z, s[g]);
-                s[g] = fmaf(x[i + 3], y.w, s[g]);
+                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(q + g * d + c * kPer + i);
+                sum[g] = fma2(x[i / 2], y.x, sum[g]);
+                sum[g] = fma2(x[i / 2 + 1], y.y, sum[g]);
             }
         }
+    }
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+        const float2 v = halves(sum[g]);
+        s[g] = v.x + v.y;
     }
 #pragma unroll
     for (int o = NT; o < 32; o <<= 1)
@@ -301,7 +334,7 @@ struct CoresetSmem {
         const int stages = WARPS * 2 * stage, merge = WARPS * RG * (dv + 2) * 4;
         q = ((stages > merge ? stages : merge) + 15) / 16 * 16;
         p = q + RG * d * 4;
-        total = p + WARPS * NT * RG * 4;
+        total = p + WARPS * NT * RG * 8;
     }
 };
 
@@ -329,7 +362,7 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
     const CoresetSmem<NT, RG, WARPS> L(s.d, s.dv, sizeof(T));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* q = reinterpret_cast<float*>(smem + L.q);
-    float* p = reinterpret_cast<float*>(smem + L.p) + warp * NT * RG;
+    uint64_t* p = reinterpret_cast<uint64_t*>(smem + L.p) + warp * NT * RG;   // a step's weights, each twice
     char* stages = smem + warp * 2 * L.stage;
     const int split = index % a.csplits, unit = index / a.csplits;
     const int rt = unit % a.row_tiles, h = unit / a.row_tiles % s.hkv, b = unit / a.row_tiles / s.hkv;
@@ -363,13 +396,14 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
     load(0, at);
     load_queries<T, RG, WARPS>(a, b, h * s.group + rt * a.rows, rows, q);
     __syncthreads();
-    float m[RG], l[RG], o[RG][COLS];
+    float m[RG], l[RG];
+    uint64_t o[RG][COLS / 2];   // columns lane + 64 i and 32 further on
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
         m[g] = -CUDART_INF_F;
         l[g] = 0.f;
 #pragma unroll
-        for (int i = 0; i < COLS; ++i) o[g][i] = 0.f;
+        for (int i = 0; i < COLS / 2; ++i) o[g][i] = 0;
     }
     for (int stage = 0; at < last; at += WARPS * NT, stage ^= 1) {
         load(stage ^ 1, at + WARPS * NT);
@@ -391,34 +425,28 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
                 m[g] = top;
                 l[g] *= f;
 #pragma unroll
-                for (int i = 0; i < COLS; ++i) o[g][i] *= f;
+                for (int i = 0; i < COLS / 2; ++i) o[g][i] = mul2(o[g][i], pair_of(f, f));
             }
             const float w = ex2(v - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
-            if (lane < NT) p[key * RG + g] = w;
+            if (lane < NT) p[key * RG + g] = pair_of(w, w);
         }
         __syncwarp();
 #pragma unroll 4
         for (int j = 0; j < live; ++j) {
             const float* w = wrows + j * (s.dv + 1);
-            float y[COLS], e[RG];
+            uint64_t y[COLS / 2];
 #pragma unroll
-            for (int i = 0; i < COLS; ++i) y[i] = lane + 32 * i < s.dv ? w[lane + 32 * i] : 0.f;
+            for (int i = 0; i < COLS / 2; ++i) {
+                const int c = lane + 64 * i;
+                y[i] = pair_of(c < s.dv ? w[c] : 0.f, c + 32 < s.dv ? w[c + 32] : 0.f);
+            }
             const float z = w[s.dv];
 #pragma unroll
-            for (int g = 0; g < RG; g += 4) {
-                if (RG % 4 == 0) {
-                    const float4 v = *reinterpret_cast<const float4*>(p + j * RG + g);
-                    e[g] = v.x, e[(g + 1) % RG] = v.y, e[(g + 2) % RG] = v.z, e[(g + 3) % RG] = v.w;
-                } else {
-#pragma unroll
-                    for (int k = g; k < RG; ++k) e[k] = p[j * RG + k];
-                }
-            }
-#pragma unroll
             for (int g = 0; g < RG; ++g) {
-                l[g] = fmaf(e[g], z, l[g]);
+                const uint64_t e = p[j * RG + g];
+                l[g] = fmaf(halves(e).x, z, l[g]);
 #pragma unroll
-                for (int i = 0; i < COLS; ++i) o[g][i] = fmaf(e[g], y[i], o[g][i]);
+                for (int i = 0; i < COLS / 2; ++i) o[g][i] = fma2(e, y[i], o[g][i]);
             }
         }
         __syncwarp();
@@ -431,8 +459,12 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
     for (int g = 0; g < RG; ++g) {
         float* row = merge + (warp * RG + g) * ld;
 #pragma unroll
-        for (int i = 0; i < COLS; ++i)
-            if (lane + 32 * i < s.dv) row[lane + 32 * i] = o[g][i];
+        for (int i = 0; i < COLS / 2; ++i) {
+            const float2 v = halves(o[g][i]);
+            const int c = lane + 64 * i;
+            if (c < s.dv) row[c] = v.x;
+            if (c + 32 < s.dv) row[c + 32] = v.y;
+        }
         if (lane == 0) {
             row[s.dv] = m[g];
             row[s.dv + 1] = l[g];
@@ -452,7 +484,7 @@ constexpr int kSimtStages = 2;
 template <int DP> using SimtRing = Ring<kSimtKeys, DP, 4, kSimtStages>;
 template <int DP, int RG>
 struct SimtSmem {
-    static constexpr int q = SimtRing<DP>::kBytes, p = q + RG * DP * 4, warp = p + kSimtKeys * RG * 4;
+    static constexpr int q = SimtRing<DP>::kBytes, p = q + RG * DP * 4, warp = p + kSimtKeys * RG * 8;
     static constexpr int total = kSimtWarps * warp;
 };
 
@@ -470,7 +502,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     char* mem = smem + warp * L::warp;
     float* q = reinterpret_cast<float*>(mem + L::q);
-    float* p = reinterpret_cast<float*>(mem + L::p);
+    uint64_t* p = reinterpret_cast<uint64_t*>(mem + L::p);   // a step's weights, each twice (as a pair)
     const int step = (s.B + kPlaces - 1) / kPlaces;
     const Place at = scan_tiles<kSimtWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, -1, pre, step,
                                                   a.status, place_sh);
@@ -506,13 +538,14 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
             const int g = i / DP, col = i % DP;
             q[i] = g < rows && col < s.d ? src[g * a.q_head + col] * a.qscale : 0.f;
         }
-        float m[RG], l[RG], o[RG][kCols * 4];
+        float m[RG], l[RG];
+        uint64_t o[RG][kCols * 2];
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
             m[g] = -CUDART_INF_F;
             l[g] = 0.f;
 #pragma unroll
-            for (int i = 0; i < kCols * 4; ++i) o[g][i] = 0.f;
+            for (int i = 0; i < kCols * 2; ++i) o[g][i] = 0;
         }
         for (int at_k = start; at_k < last; ++at_k) {
         fetch(stage ^ 1);
@@ -521,21 +554,25 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
         __syncwarp();
         const char* krows = mem + stage * SimtRing<DP>::kStage;
         const char* vrows = krows + KEYS * SimtRing<DP>::kRow;
-        float x[RG];
+        uint64_t xx[RG];
 #pragma unroll
-        for (int g = 0; g < RG; ++g) x[g] = 0.f;
+        for (int g = 0; g < RG; ++g) xx[g] = 0;
 #pragma unroll 8
         for (int i = 0; i < kChunks / 4; ++i) {
             const int ch = part + 4 * i;
-            const float4 k4 = *reinterpret_cast<const float4*>(krows + key * SimtRing<DP>::kRow + (ch ^ key) * 16);
+            const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(krows + key * SimtRing<DP>::kRow + (ch ^ key) * 16);
 #pragma unroll
             for (int g = 0; g < RG; ++g) {
-                const float4 q4 = *reinterpret_cast<const float4*>(q + g * DP + ch * 4);
-                x[g] = fmaf(k4.x, q4.x, x[g]);
-                x[g] = fmaf(k4.y, q4.y, x[g]);
-                x[g] = fmaf(k4.z, q4.z, x[g]);
-                x[g] = fmaf(k4.w, q4.w, x[g]);
+                const ulonglong2 q4 = *reinterpret_cast<const ulonglong2*>(q + g * DP + ch * 4);
+                xx[g] = fma2(k4.x, q4.x, xx[g]);
+                xx[g] = fma2(k4.y, q4.y, xx[g]);
             }
+        }
+        float x[RG];
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            const float2 v = halves(xx[g]);
+            x[g] = v.x + v.y;
         }
         const bool ok = (mask >> key) & 1;
         const int pos = at_k * KEYS + key;
@@ -554,32 +591,30 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
                 m[g] = top;
                 l[g] *= f;
 #pragma unroll
-                for (int i = 0; i < kCols * 4; ++i) o[g][i] *= f;
+                for (int i = 0; i < kCols * 2; ++i) o[g][i] = mul2(o[g][i], pair_of(f, f));
             }
             // nothing but masked keys so far: the reference is 0, every weight 2^-inf = 0
             const float w = ex2(x[g] - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
             if (part == 0) {
                 l[g] += w;
-                p[key * RG + g] = w;
+                p[key * RG + g] = pair_of(w, w);
             }
         }
         __syncwarp();
 #pragma unroll
         for (int j0 = 0; j0 < KEYS; j0 += kGroups) {
             const int j = j0 + (kGroups > 1 ? lane / kChunks : 0);
-            float w[RG];
+            uint64_t w[RG];
 #pragma unroll
             for (int g = 0; g < RG; ++g) w[g] = p[j * RG + g];
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
                 const int ch = (kGroups > 1 ? lane % kChunks : lane) + n * 32;
-                const float4 y = *reinterpret_cast<const float4*>(vrows + j * SimtRing<DP>::kRow + (ch ^ (j & 7)) * 16);
+                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(vrows + j * SimtRing<DP>::kRow + (ch ^ (j & 7)) * 16);
 #pragma unroll
                 for (int g = 0; g < RG; ++g) {
-                    o[g][n * 4] = fmaf(w[g], y.x, o[g][n * 4]);
-                    o[g][n * 4 + 1] = fmaf(w[g], y.y, o[g][n * 4 + 1]);
-                    o[g][n * 4 + 2] = fmaf(w[g], y.z, o[g][n * 4 + 2]);
-                    o[g][n * 4 + 3] = fmaf(w[g], y.w, o[g][n * 4 + 3]);
+                    o[g][n * 2] = fma2(w[g], y.x, o[g][n * 2]);
+                    o[g][n * 2 + 1] = fma2(w[g], y.y, o[g][n * 2 + 1]);
                 }
             }
         }
@@ -592,10 +627,16 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
         for (int g = 0; g < RG; ++g) {
 #pragma unroll
             for (int e = 1; e < 32; e <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], e);
+            float v[kCols * 4];
+#pragma unroll
+            for (int i = 0; i < kCols * 2; ++i) {
+                const float2 u = halves(o[g][i]);
+                v[2 * i] = u.x, v[2 * i + 1] = u.y;
+            }
 #pragma unroll
             for (int e = 32 / kGroups; e < 32; e <<= 1)
 #pragma unroll
-                for (int i = 0; i < kCols * 4; ++i) o[g][i] += __shfl_xor_sync(0xffffffffu, o[g][i], e);
+                for (int i = 0; i < kCols * 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], e);
             if (g >= rows) continue;
             const bool none = nothing(m[g], l[g]);
             float* to = whole ? a.out + (row0 + g) * s.dv : a.parts + (part_row + g) * s.dv;
@@ -604,8 +645,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
                 const int col = (lane + n * 32) * 4;
                 if (lane < 32 / kGroups && col < s.dv)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        to[col + e] = whole ? (none ? 0.f : o[g][n * 4 + e] / l[g]) : o[g][n * 4 + e];
+                    for (int e = 0; e < 4; ++e) to[col + e] = whole ? (none ? 0.f : v[n * 4 + e] / l[g]) : v[n * 4 + e];
             }
             if (lane == 0) {
                 if (!whole) a.parts_lm[part_row + g] = make_float2(l[g], m[g]);
@@ -663,23 +703,6 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t t[3]) {
         x -= __uint_as_float(t[i] << 16);
         y -= __uint_as_float(t[i] & 0xffff0000u);
     }
-}
-
-// Pairs of fp32 values in one 64-bit register, added and multiplied as one.
-__device__ __forceinline__ uint64_t pair_of(float x, float y) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-    uint64_t p;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
-    return p;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-    uint64_t p;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(x), "l"(y));
-    return p;
 }
 
 constexpr int kMmaKeys = 16;     // keys of one warp's step
@@ -977,17 +1000,18 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
     __shared__ float red[kJoinWarps];
     __shared__ float refs[kScoreRows][2];
     const View& s = a.s;
-    const int per_tile = s.hkv * a.row_tiles, dv = s.dv, slices = (dv + cols - 1) / cols;
+    const int per_tile = s.hkv * a.row_tiles, dv = s.dv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row_blocks = s.B * s.hq * slices;
+    const int per_seq = cols ? s.hq * ((dv + cols - 1) / cols) : (s.hq + kJoinWarps - 1) / kJoinWarps;
+    const int row_blocks = s.B * per_seq;
     const bool score = (int)blockIdx.x >= row_blocks;
     const int chunks = (s.cap + kScoreKeys - 1) / kScoreKeys;
     int b, hq0, key0 = 0, col0 = 0;
     if (!score) {
-        const int row = blockIdx.x / slices;
-        col0 = (blockIdx.x - row * slices) * cols;
-        b = row / s.hq;
-        hq0 = row - b * s.hq;
+        b = blockIdx.x / per_seq;
+        const int i = blockIdx.x - b * per_seq;
+        hq0 = cols ? i % s.hq : i * kJoinWarps + warp;
+        col0 = cols ? i / s.hq * cols : 0;
     } else {
         const int i = blockIdx.x - row_blocks, unit = i / chunks;
         b = unit / s.hkv;
@@ -1019,9 +1043,51 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
     auto lm = [&](int i) {   // (normaliser, reference) of a set
         return *(i < n_pages ? a.parts_lm + page0 + (int64_t)i * a.rows : a.cparts_lm + core0 + (int64_t)(i - n_pages) * a.rows);
     };
-    const bool to_join = score || find_sets(hq0);
+    const bool to_join = score || (hq0 < s.hq && find_sets(hq0));
     grid_dependency_wait();   // the partial rows (and everything before them) are there from here on
     if (!to_join) return;
+    // a warp's reference and normaliser over all sets, in an order that the number of sets alone decides
+    auto totals = [&](float& m, float& l) {
+        m = -CUDART_INF_F;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, lm(i).y);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        l = 0.f;
+#pragma unroll 4
+        for (int i = lane; i < n; i += 32) {
+            const float2 v = lm(i);
+            l = fmaf(ex2(v.y - ref), v.x, l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    };
+    const int64_t step = (int64_t)a.rows * dv;
+    if (!score && !cols) {
+        float m, l;
+        totals(m, l);
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        const int64_t row = (int64_t)b * s.hq + hq0;
+        const bool empty = nothing(m, l);
+        for (int col = lane * 4; col < dv; col += 128) {
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float* rows_p = a.parts + page0 * dv + col;
+            const float* rows_c = a.cparts + core0 * dv + col;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float f = ex2(lm(i).y - ref);
+                const float4 v = *reinterpret_cast<const float4*>(i < n_pages ? rows_p + i * step
+                                                                              : rows_c + (i - n_pages) * step);
+                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
+            float* to = a.out + row * dv + col;
+            to[0] = empty ? 0.f : o.x / l, to[1] = empty ? 0.f : o.y / l;
+            to[2] = empty ? 0.f : o.z / l, to[3] = empty ? 0.f : o.w / l;
+        }
+        if (lane == 0 && a.lse) a.lse[row] = log_sum(m, l);
+        return;
+    }
     if (!score) {
         // the maximum over all sets
         float m = -CUDART_INF_F;
@@ -1051,7 +1117,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
             if (in) {
                 const float* rows_p = a.parts + page0 * dv + col;
                 const float* rows_c = a.cparts + core0 * dv + col;
-                const int64_t step = (int64_t)a.rows * dv;
 #pragma unroll 4
                 for (int i = sg; i < held; i += groups) {
                     const int j = i0 + i;
@@ -1096,23 +1161,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
         __syncthreads();
         for (int r = warp; r < rows; r += kJoinWarps) {
             find_sets(hq0 + r0 + r);
-            float m = -CUDART_INF_F, l = 0.f;
-            for (int i = lane; i < n; i += 32) m = fmaxf(m, lm(i).y);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float ref = m == -CUDART_INF_F ? 0.f : m;
-            for (int i = lane; i < n; i += 32) {
-                const float2 v = lm(i);
-                l = fmaf(ex2(v.y - ref), v.x, l);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            float m, l;
+            totals(m, l);
             if (lane == 0) {
-                refs[r][0] = ref;
+                refs[r][0] = m == -CUDART_INF_F ? 0.f : m;
                 refs[r][1] = nothing(m, l) ? 0.f : 1.f / l;   // no weight anywhere: 0 for every key
             }
         }
         __syncthreads();
+#pragma unroll 4
         for (int r = 0; r < rows; ++r) {
             const float* x = a.logits + ((int64_t)b * s.hq + hq0 + r0 + r) * s.cap;
             const float ref = refs[r][0], inv = refs[r][1];
@@ -1180,10 +1237,14 @@ wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel 
     if (resident_blocks(reinterpret_cast<const void*>(pages), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
     const int64_t units = (int64_t)a.s.B * a.s.hkv * a.row_tiles, most = units * ((a.s.cap + tile - 1) / tile);
     const int64_t chunks = (a.s.cap + kScoreKeys - 1) / kScoreKeys, rows = (int64_t)a.s.B * a.s.hq;
-    // a block for 32 columns of a row while that is what fills the GPU, else for all of the row's
-    int cols = 32;
-    while (cols < a.s.dv && rows * ((a.s.dv + cols - 1) / cols) > 4 * 148) cols *= 2;
-    const int64_t join = rows * ((a.s.dv + cols - 1) / cols) + (a.scores ? chunks * a.s.B * a.s.hkv : 0);
+    // Where the rows are at most the blocks that the GPU holds at once, a block for as few columns (32 and up) of
+    // a row as that allows (32 rows of 150 sets each: 3 us against 8 for a warp a row); where they are more, a
+    // warp for a row (1024 rows of 5 sets: 7 us against 9).
+    const int64_t most_blocks = 4 * 148;
+    int cols = rows <= most_blocks ? 32 : 0;
+    while (cols && cols < a.s.dv && rows * ((a.s.dv + cols - 1) / cols) > most_blocks) cols *= 2;
+    const int64_t join = (cols ? rows * ((a.s.dv + cols - 1) / cols) : (int64_t)a.s.B * ((a.s.hq + kJoinWarps - 1) / kJoinWarps)) +
+                         (a.scores ? chunks * a.s.B * a.s.hkv : 0);
     if (most > INT32_MAX || join > INT32_MAX) return WC_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
     if (a.csplits) {
         if (units * a.csplits > INT32_MAX) return WC_ERR_UNSUPPORTED;
