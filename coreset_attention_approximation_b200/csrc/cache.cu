@@ -273,7 +273,7 @@ __device__ __forceinline__ int block_scan(int v, int* sh) {
 // largest of those that compete) comes from a radix select in three passes (11,
 // 11 and 10 bits of the ordered keys): each block counts its own keys, every
 // block adds the cluster's histograms through distributed shared memory and
-// finds the same bin.  Then each warp counts what it keeps of its own stretch,
+// finds the same bin; a bin that is kept whole ends the search.  Then each warp counts what it keeps of its own stretch,
 // and writes the positions in order behind those of the warps before it.  The
 // keys are read from memory once and held in shared memory where they fit.
 // Bound by the latency of the passes (a few barriers each) for the lengths of
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
     __shared__ int2 counts[kSelectWarps];
     __shared__ int2 block_counts;
     __shared__ uint32_t s_bin;
-    __shared__ int s_left;
+    __shared__ int s_left, s_whole;
     grid_dependency_wait();
     grid_dependents_launch();
     namespace cg = cooperative_groups;
@@ -326,11 +326,13 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
         for (int i = lo + tid; i < hi; i += kSelectThreads) keys[i - lo] = score_key(x[i]);
     uint32_t prefix = 0, mask = 0;
     int left = want;
+    bool whole = false;
     __syncthreads();
     if (want > 0) {
         const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
 #pragma unroll
         for (int pass = 0; pass < 3; ++pass) {
+            if (whole) break;   // (the same in every block: each added the same counts)
             const int bins = 1 << bits[pass];
             for (int i = max(lo, first) + tid; i < min(hi, last); i += kSelectThreads) {
                 const uint32_t k = key(i);
@@ -368,6 +370,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
                     if (before < left && left <= before + n[i]) {
                         s_bin = low + i;
                         s_left = left - before;
+                        s_whole = left - before == n[i];
                     }
                     before += n[i];
                 }
@@ -376,9 +379,11 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
             prefix |= s_bin << shifts[pass];
             mask |= (uint32_t)(bins - 1) << shifts[pass];
             left = s_left;
+            whole = s_whole != 0;   // all of the bin are kept: its keys need not be told apart (mostly after two passes)
         }
     }
-    // kept: the positions that do not compete, the keys above `prefix`, and the first `left` equal to it
+    // kept: the positions that do not compete, the keys above `prefix` and, of those equal to it, the first
+    // `left`, or, where the bin is kept whole, the keys from `prefix` up
     const int span = ((hi - lo + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
     const int w0 = min(lo + warp * span, hi), w1 = min(w0 + span, hi);
     auto judge = [&](int i, bool& above, bool& tie) {
@@ -387,8 +392,8 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
         if (i < first || i >= last) above = true;
         else if (want > 0) {
             const uint32_t k = key(i);
-            above = k > prefix;
-            tie = k == prefix;
+            above = whole ? k >= prefix : k > prefix;
+            tie = !whole && k == prefix;
         }
     };
     int n_above = 0, n_tie = 0;

@@ -474,14 +474,14 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
     join_warps<RG, WARPS>(a, merge, index, rows);
 }
 
-// fp32 pages, on CUDA cores (their products keep 24 bits): 8 keys a step, two
-// stages a warp.  For the logits a lane holds one key and a quarter of the
+// fp32 pages, on CUDA cores (their products keep 24 bits): 8 keys a step, two or
+// three stages a warp.  For the logits a lane holds one key and a quarter of the
 // width, for the values four columns (and, where fewer than 32 lanes cover the
 // width, every second key).  DP: d and dv rounded up to 64, 128 or 256.
 constexpr int kSimtKeys = 8;
-constexpr int kSimtStages = 2;
+template <int DP> constexpr int kSimtStages = DP > 64 ? 2 : 3;
 
-template <int DP> using SimtRing = Ring<kSimtKeys, DP, 4, kSimtStages>;
+template <int DP> using SimtRing = Ring<kSimtKeys, DP, 4, kSimtStages<DP>>;
 template <int DP, int RG>
 struct SimtSmem {
     static constexpr int q = SimtRing<DP>::kBytes, p = q + RG * DP * 4, warp = p + kSimtKeys * RG * 8;
@@ -512,11 +512,12 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
     ahead = now;
     SimtRing<DP> ring;
     ring.init(a, mem);
+    constexpr int kStages = kSimtStages<DP>;
     uint32_t masks = 0;   // the live keys of the steps in the ring, a byte each, the next one lowest after a fetch
     auto fetch = [&](int stage) {   // the next step's copies; where the one after it is
         masks >>= 8;
         if (ahead.left > 0) {
-            masks |= ring.fetch(a, stage) << 8;
+            masks |= ring.fetch(a, stage) << (8 * (kStages - 1));
             if (ahead.skip(a, 1, KEYS)) ring.enter(a, ahead);
             ring.locate(a, ahead);
         }
@@ -524,7 +525,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
     };
     ring.enter(a, ahead);
     ring.locate(a, ahead);
-    fetch(0);
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
     const int key = lane % KEYS, part = lane / KEYS;
     int stage = 0;
     while (now.left > 0) {
@@ -548,10 +550,10 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
             for (int i = 0; i < kCols * 2; ++i) o[g][i] = 0;
         }
         for (int at_k = start; at_k < last; ++at_k) {
-        fetch(stage ^ 1);
-        const uint32_t mask = masks & 0xff;
-        cp_async_wait<1>();
+        cp_async_wait<kStages - 2>();
         __syncwarp();
+        fetch(stage == 0 ? kStages - 1 : stage - 1);   // the stage that the last step read is free
+        const uint32_t mask = masks & 0xff;
         const char* krows = mem + stage * SimtRing<DP>::kStage;
         const char* vrows = krows + KEYS * SimtRing<DP>::kRow;
         uint64_t xx[RG];
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
             }
         }
         __syncwarp();
-        stage ^= 1;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         }
         // finished rows where the share is the whole unit, else partial rows
         const bool whole = start == 0 && last == now.tiles && !a.csplits && !a.logits;
