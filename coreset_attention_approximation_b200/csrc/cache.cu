@@ -175,14 +175,14 @@ __global__ void __launch_bounds__(kCopyThreads) cache_append_kernel(const Append
          i += (int64_t)gridDim.x * (kCopyThreads / 32)) {
         const int64_t unit = i / groups;
         const int j = (int)(i - unit * groups) * kCopyRows + lane, b = (int)(unit / s.hkv), h = (int)(unit - (int64_t)b * s.hkv);
-        int n = a.count ? __ldg(a.count + b) : a.t;
+        int n = a.count ? a.count[b] : a.t;
         if (n < 0 || n > a.t) {
             record_status(a.status, WC_ERR_BOUNDS);
             n = min(max(n, 0), a.t);
         }
         RowCopy r{nullptr, nullptr, nullptr, nullptr, false};
         if (lane < kCopyRows && j < n) {
-            const int64_t at = (int64_t)__ldg(a.pos + b) + j;
+            const int64_t at = (int64_t)a.pos[b] + j;
             if (at < 0 || at >= s.cap) {
                 record_status(a.status, WC_ERR_BOUNDS);
             } else {
@@ -646,7 +646,7 @@ wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const
     AppendArgs a{};
     wc_status e = make_view(cache, &a.s);
     if (e != WC_OK) return e;
-    if (t < 0) return WC_ERR_INVALID;
+    if (t < 0 || t > (1 << 30)) return WC_ERR_INVALID;
     if (!pos || !k || !v || !table || !aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 4) || !aligned(count, 4) ||
         !aligned(table, 4) || !aligned(scores, 4))
         return WC_ERR_INVALID;

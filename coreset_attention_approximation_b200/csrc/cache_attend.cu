@@ -217,7 +217,7 @@ struct Ring {
         keys = min(KEYS, w.len - first);
         const int tp = page_of(s, min(key, w.len - 1));
         slot = key - tp * s.page;
-        page = __ldg(s.table + (int64_t)w.b * s.max_pages + tp);
+        page = s.table[(int64_t)w.b * s.max_pages + tp];
     }
     // Starts the copies of the located step and returns a bit for each key that
     // is there.  A value row that is not is filled with zeros (its weight is 0,
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
     const int split = index % a.csplits, unit = index / a.csplits;
     const int rt = unit % a.row_tiles, h = unit / a.row_tiles % s.hkv, b = unit / a.row_tiles / s.hkv;
     const int rows = min(a.rows, s.group - rt * a.rows);
-    int n = a.rank ? __ldg(a.rank + b * s.hkv + h) : a.r;
+    int n = a.rank ? a.rank[b * s.hkv + h] : a.r;
     if (n < 0 || n > a.r) {
         record_status(a.status, WC_ERR_BOUNDS);
         n = n < 0 ? 0 : a.r;

@@ -88,7 +88,7 @@ bool launch(void (*kern)(A...), int64_t grid, int threads, int smem, cudaStream_
 
 // A sequence's length, held to [0, cap]; one outside is recorded.
 __device__ __forceinline__ int checked_len(const int32_t* lens, int b, int cap, int* status) {
-    int n = __ldg(lens + b);
+    int n = lens[b];
     if (n < 0 || n > cap) {
         record_status(status, WC_ERR_BOUNDS);
         n = n < 0 ? 0 : cap;
@@ -103,7 +103,7 @@ __device__ __forceinline__ int page_of(const View& s, int t) {
 
 // Page of token t of sequence b, or -1 (recorded) where the table's entry is no page.
 __device__ __forceinline__ int checked_page(const View& s, const int32_t* table, int b, int t_page, int* status) {
-    const int p = __ldg(table + (int64_t)b * s.max_pages + t_page);
+    const int p = table[(int64_t)b * s.max_pages + t_page];
     if ((unsigned)p >= (unsigned)s.n_pages) {
         record_status(status, WC_ERR_BOUNDS);
         return -1;
@@ -130,7 +130,9 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Programmatic dependent launch: lets the stream's next kernel start its
-// blocks, and waits until the kernel before this one is complete.
+// blocks, and waits until the kernel before this one is complete.  (No load of
+// these kernels is a read-only-cache load: the compiler may move such a load up
+// past the wait.)
 __device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -379,7 +379,8 @@ class PagedCache:
     Lengths, positions and counts are int32 CUDA tensors that the caller keeps
     and advances, so a captured graph serves a growing cache.  The tensors
     given here are kept by reference and changed in place.  Lengths and page
-    numbers are checked on the device (`check()` reports).  The cache's calls
+    numbers are checked on the device (`check()` reports).  To use other
+    tensors, make another PagedCache.  The cache's calls
     share one workspace: calls that may overlap on the GPU (two streams, two
     graphs replayed at once) need a PagedCache each.
 

@@ -59,6 +59,17 @@ def test_invalid_caches_are_refused_by_every_call(lib, kw):
     assert lib.wc_cache_evict(ctypes.byref(s), 5, 0, 0, OK, OK, OK, None, OK, OK, None, OK, OK, OK, BIG, None) == 1
 
 
+def test_strides_beyond_32_bits_are_unsupported(lib):
+    for kw in (dict(k_page=1 << 31), dict(v_page=1 << 32), dict(k_token=1 << 31, k_head=64)):
+        s = shape(**dict(DENSE, **kw))
+        assert lib.wc_cache_workspace_bytes(ctypes.byref(s), 0) == 0
+        assert lib.wc_cache_attend(ctypes.byref(s), OK, 512, 64, OK, OK, OK, OK, 0, None, None, None, OK, OK, OK, OK,
+                                   BIG, None) == 4
+    # heads may lie further apart
+    s = shape(**dict(DENSE, k_head=1 << 33, v_head=1 << 33))
+    assert lib.wc_cache_workspace_bytes(ctypes.byref(s), 0) > 0
+
+
 def test_append_refusals(lib):
     s, r = shape(), wildcat.WcRowStrides(128, 64, 64)
 
@@ -67,7 +78,7 @@ def test_append_refusals(lib):
         return lib.wc_cache_append(ctypes.byref(s), t, K, ref(ks), V, ref(vs), pos, count, k, v, table, scores, ws, n,
                                    None)
 
-    assert call(t=-1) == 1
+    assert call(t=-1) == 1 and call(t=(1 << 30) + 1) == 1
     for name in ("K", "ks", "V", "vs", "pos", "k", "v", "table", "ws"):
         assert call(**{name: None}) == 1, name
     for name in ("K", "V", "k", "v", "ws"):
@@ -94,6 +105,7 @@ def test_attend_refusals(lib):
     assert call(out=ctypes.c_void_p((1 << 20) + 2)) == 1
     assert call(r=-1) == 1 and call(r=4097, Ks=OK, W=OK) == 1
     assert call(r=4, W=OK) == 1 and call(r=4, Ks=OK) == 1 and call(r=4, Ks=ODD, W=OK) == 1
+    assert call(r=4, Ks=OK, W=ODD) == 1
     small = lib.wc_cache_workspace_bytes(ctypes.byref(s), 0)
     assert call(n=small - 1) == 5
     assert call(scores=OK, n=small) == 5           # accumulation needs the larger workspace

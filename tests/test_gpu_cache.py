@@ -99,6 +99,14 @@ def test_attend_lengths(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_attend_thousands_of_sequences(dtype):
+    """More sequences than a block holds places for."""
+    lens = [(7 * i) % 23 if i % 5 else 0 for i in range(2500)] + [90] + [0] * 30
+    case = Case(dtype, len(lens), 2, 1, 16, 16, 8, 12, lens, seed=24)
+    check_attend(case)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_attend_without_scores_and_lse(dtype):
     case = Case(dtype, 3, 8, 2, 64, 64, 16, 40, [640, 100, 0], seed=5)
     check_attend(case, accumulate=False)
@@ -373,6 +381,117 @@ def test_evict_long(n):
     case.scores[0, 0] = torch.exp(3 * torch.randn(case.cap))
     case.scores[0, 1, 100:] = 0.0
     check_evict(case, 9000, 4, 500, False, False)
+
+
+def test_evict_again_and_again():
+    """Calls one after the other, in place (given as such, or by the table
+    itself), with refusals between them: no count of pages is left over."""
+    case = Case(BF, 2, 2, 2, 64, 64, 16, 30, [470, 200], seed=25)
+    cache, _, lens = make(case)
+    for keep, into in ((300, None), (250, cache.table), (250, None), (100, None), (99, cache.table), (3, None)):
+        before = cache.scores.cpu().clone()
+        n = lens.tolist()
+        res = cache.evict(lens, keep, recent=2, into=into, lens_out=lens)
+        assert cache.check() == 0 and lens.tolist() == [min(x, keep) for x in n]
+        for b in range(2):
+            for h in range(2):
+                want = cache_ref.kept_positions(before[b, h].numpy(), n[b], keep, 0, 2)
+                assert np.array_equal(res["idx"][b, h, : len(want)].cpu().numpy(), want)
+        if keep == 250:
+            good = cache.table.clone()
+            cache.table[1, 0] = cache.table[0, 0]
+            left = lens.tolist()
+            cache.evict(lens, 20, lens_out=lens)
+            assert cache.check() == 1 and lens.tolist() == left
+            cache.table.copy_(good)
+
+
+def test_evict_captured():
+    """Captured once, replayed on restored scores: the same kept positions as
+    an eager call, whichever call came before."""
+    case = Case(F32, 2, 2, 2, 64, 64, 16, 30, [470, 200], seed=26)
+    cache, _, lens = make(case)
+    k, v, sc = cache.k_pages.clone(), cache.v_pages.clone(), cache.scores.clone()
+    want = cache.evict(lens, 70, sink=1, recent=9)
+    after = plain(cache.k_pages), plain(cache.v_pages), cache.scores.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.k_pages.copy_(k), cache.v_pages.copy_(v), cache.scores.copy_(sc)
+        res = cache.evict(lens, 70, sink=1, recent=9)
+    for i in range(4):
+        graph.replay()
+        assert torch.equal(res["idx"], want["idx"]) and torch.equal(res["lens"], want["lens"])
+        assert torch.equal(plain(cache.k_pages), after[0]) and torch.equal(plain(cache.v_pages), after[1])
+        assert torch.equal(cache.scores, after[2])
+        if i == 1:
+            cache.evict(lens, 300)
+    assert cache.check() == 0
+
+
+def test_pools_beyond_four_gigabytes():
+    """Pages whose offsets pass 32 bits, in bytes and in elements: append,
+    attention and eviction there."""
+    page, d, n_pages, top = 65536, 128, 560, 555          # 16 MiB a page; 9 GiB of keys and 9 of values
+    k = torch.empty(n_pages, 1, page, d, dtype=BF, device="cuda")
+    v = torch.empty(n_pages, 1, page, d, dtype=BF, device="cuda")
+    table = torch.tensor([[top, 3], [256, 400]], dtype=torch.int32, device="cuda")
+    scores = torch.zeros(2, 1, 2 * page, device="cuda")
+    cache = wildcat.PagedCache(k, v, table, hq=4, scores=scores)
+    g = torch.Generator().manual_seed(3)
+    n = 300
+    K, V = (torch.randn(2, 1, n, d, generator=g).to(BF) for _ in range(2))
+    Q = torch.randn(2, 4, d, generator=g).to(BF)
+    pos = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    cache.append(K.cuda(), V.cuda(), pos)
+    cache.append(K.cuda()[:, :, :5], V.cuda()[:, :, :5], torch.zeros_like(pos), torch.tensor([0, 5], dtype=torch.int32).cuda())
+    lens = torch.tensor([n, n + 5], dtype=torch.int32, device="cuda")
+    assert torch.equal(k[top, 0, :n].cpu(), K[0, 0]) and torch.equal(v[256, 0, 5:n + 5].cpu(), V[1, 0])
+    out = cache.attend(Q.cuda(), lens, accumulate=True)
+    for b in range(2):
+        kk = K[b, 0] if b == 0 else torch.cat([K[b, 0, :5], K[b, 0]])
+        vv = V[b, 0] if b == 0 else torch.cat([V[b, 0, :5], V[b, 0]])
+        p = torch.softmax(Q[b].double() @ kk.double().T / math.sqrt(d), -1)
+        # the fp32 bound of cache_ref.attend for these sizes: 128 products of at most 20 in all, 305 keys
+        assert float((out[b].cpu().double() - p @ vv.double()).abs().max()) <= 2 ** -23 * (15.4 * 20 + 34) * 5
+        res = cache.scores[b, 0, : len(kk)].cpu().double() - p.sum(0)
+        assert float(res.abs().max()) <= 2 ** -23 * (15.4 * 20 + 34) * 4
+    idx = cache.evict(lens, 40)["idx"].cpu().long()
+    assert cache.check() == 0
+    assert torch.equal(k[top, 0, :40].cpu(), K[0, 0][idx[0, 0]])
+    assert torch.equal(v[256, 0, :40].cpu(), torch.cat([V[1, 0, :5], V[1, 0]])[idx[1, 0]])
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured, with nothing run before."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+from coreset_attention_approximation_b200 import wildcat
+k = torch.randn(8, 2, 16, 64, device="cuda").bfloat16()
+table = torch.arange(8, dtype=torch.int32, device="cuda").reshape(2, 4)
+scores = torch.zeros(2, 2, 64, device="cuda")
+cache = wildcat.PagedCache(k, k.clone(), table, hq=4, scores=scores)
+q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+new = torch.randn(2, 2, 1, 64, device="cuda").bfloat16()
+lens = torch.tensor([50, 7], dtype=torch.int32, device="cuda")
+core = (torch.randn(2, 2, 9, 64, device="cuda").bfloat16(), torch.rand(2, 2, 9, 65, device="cuda"), None)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    cache.append(new, new, lens)
+    out = cache.attend(q, lens, coreset=core, accumulate=True)
+    res = cache.evict(lens, 20)
+g.replay()
+torch.cuda.synchronize()
+assert cache.check() == 0 and res["lens"].tolist() == [20, 7] and bool(torch.isfinite(out).all())
+print("fine")
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "fine" in done.stdout, done.stderr[-2000:]
 
 
 def test_evict_extreme_scores():
