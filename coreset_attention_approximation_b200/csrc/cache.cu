@@ -278,7 +278,8 @@ __device__ __forceinline__ int block_scan(int v, int* sh) {
 // keys are read from memory once and held in shared memory where they fit.
 // Bound by the latency of the passes (a few barriers each) for the lengths of
 // real caches.
-__global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_select_kernel(const EvictArgs a, int held) {
+template <int RANKS>
+__global__ void __launch_bounds__(kSelectThreads, 3) cache_select_kernel(const EvictArgs a, int held) {
     extern __shared__ __align__(16) uint32_t keys[];
     __shared__ __align__(16) int hist[3][2048];   // (read four at a time)
     __shared__ int sh[kSelectWarps];
@@ -290,7 +291,13 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
     grid_dependents_launch();
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    constexpr int ranks = RANKS;
+    const int rank = RANKS > 1 ? (int)cluster.block_rank() : 0;
+    auto sync_all = [&] {   // the cluster's blocks
+        if (RANKS > 1) cluster.sync();
+        else __syncthreads();
+    };
+    auto of_rank = [&](auto* p, int r) { return RANKS > 1 ? cluster.map_shared_rank(p, r) : p; };
     const View& s = a.s;
     const int unit = blockIdx.x / ranks, h = unit % s.hkv, b = unit / s.hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -338,7 +345,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
                 const uint32_t k = key(i);
                 if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shifts[pass]) & (bins - 1)], 1);
             }
-            cluster.sync();
+            sync_all();
             // from the top bin down: the bin in which the `left`-th key lies; a thread has kSelectBins of
             // them, from bin `low` up, and takes every block's counts, all loads in flight
             const int low = bins - kSelectBins * (tid + 1);
@@ -348,14 +355,12 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
             if (low >= 0) {
 #pragma unroll
                 for (int i = 0; i < kSelectBins; i += 4) {
-                    int4 v[kSelectCluster];
+                    int4 v[RANKS];
 #pragma unroll
-                    for (int r = 0; r < kSelectCluster; ++r)
-                        v[r] = r < ranks ? *reinterpret_cast<const int4*>(
-                                               cluster.map_shared_rank(&hist[pass][low + i], r))
-                                         : make_int4(0, 0, 0, 0);
+                    for (int r = 0; r < RANKS; ++r)
+                        v[r] = *reinterpret_cast<const int4*>(of_rank(&hist[pass][low + i], r));
 #pragma unroll
-                    for (int r = 0; r < kSelectCluster; ++r) {
+                    for (int r = 0; r < RANKS; ++r) {
                         n[i] += v[r].x, n[i + 1] += v[r].y, n[i + 2] += v[r].z, n[i + 3] += v[r].w;
                     }
                 }
@@ -396,10 +401,13 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
             tie = !whole && k == prefix;
         }
     };
-    int n_above = 0, n_tie = 0;
-    for (int i = w0; i < w1; i += 32) {
+    // (a bit for each of the first 32 rounds keeps what was found for the second time over)
+    uint32_t were_above = 0, were_tie = 0;
+    int n_above = 0, n_tie = 0, round = 0;
+    for (int i = w0; i < w1; i += 32, ++round) {
         bool above, tie;
         judge(i + lane, above, tie);
+        if (round < 32) were_above |= (uint32_t)above << round, were_tie |= (uint32_t)tie << round;
         n_above += __popc(__ballot_sync(0xffffffffu, above));
         n_tie += __popc(__ballot_sync(0xffffffffu, tie));
     }
@@ -416,18 +424,19 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
         if (lane < kSelectWarps) counts[lane] = make_int2(c.x - own.x, c.y - own.y);
         if (lane == 31) block_counts = c;
     }
-    cluster.sync();
-    int2 blocks[kSelectCluster];
+    sync_all();
+    int2 blocks[RANKS];
 #pragma unroll
-    for (int r = 0; r < kSelectCluster; ++r)
-        blocks[r] = r < rank ? *cluster.map_shared_rank(&block_counts, r) : make_int2(0, 0);
+    for (int r = 0; r < RANKS; ++r) blocks[r] = r < rank ? *of_rank(&block_counts, r) : make_int2(0, 0);
     int above_before = counts[warp].x, ties_before = counts[warp].y;
 #pragma unroll
-    for (int r = 0; r < kSelectCluster; ++r) above_before += blocks[r].x, ties_before += blocks[r].y;
+    for (int r = 0; r < RANKS; ++r) above_before += blocks[r].x, ties_before += blocks[r].y;
     int at = above_before + min(ties_before, left);
-    for (int i = w0; i < w1; i += 32) {
+    round = 0;
+    for (int i = w0; i < w1; i += 32, ++round) {
         bool above, tie;
-        judge(i + lane, above, tie);
+        if (round < 32) above = (were_above >> round) & 1, tie = (were_tie >> round) & 1;
+        else judge(i + lane, above, tie);
         const uint32_t below = (1u << lane) - 1, ties = __ballot_sync(0xffffffffu, tie);
         const bool keep = above || (tie && ties_before + __popc(ties & below) < left);
         const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
@@ -435,7 +444,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) cache_s
         at += __popc(keeps);
         ties_before += __popc(ties);
     }
-    cluster.sync();   // no block leaves while another may read its shared memory
+    if (RANKS > 1) cluster.sync();   // no block leaves while another may read its shared memory
 }
 
 constexpr int kMoveThreads = 256;
@@ -565,15 +574,16 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArg
     else move_in_place(a, b, h, part - 1, kept, stage);
 }
 
-// The two kernels' shared-memory limits, once per device.
+// The kernels' shared-memory limits, once per device.
 wc_status evict_setup() {
     static std::atomic<uint64_t> done{0};   // a bit per device number (the first 64; the others set it each time)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return WC_ERR_CUDA;
     if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return WC_OK;
-    if (cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectHeld * 4) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(cache_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes) != cudaSuccess)
+    for (auto kern : {cache_select_kernel<1>, cache_select_kernel<2>, cache_select_kernel<4>, cache_select_kernel<8>})
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectHeld * 4) != cudaSuccess)
+            return WC_ERR_CUDA;
+    if (cudaFuncSetAttribute(cache_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes) != cudaSuccess)
         return WC_ERR_CUDA;
     if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
     return WC_OK;
@@ -583,10 +593,10 @@ wc_status launch_evict(const EvictArgs& a, cudaStream_t st) {
     const View& s = a.s;
     wc_status e = evict_setup();
     if (e != WC_OK) return e;
-    // blocks of one (sequence, kv head): one for each kSelectSlice positions, while they leave no SM without a unit
+    // blocks of one (sequence, kv head): one for each kSelectSlice positions, while there are at most four an SM
     const int64_t units = (int64_t)s.B * s.hkv;
     int ranks = 1;
-    while (ranks < kSelectCluster && 2 * ranks * units <= 2 * 148 && (int64_t)ranks * kSelectSlice < s.cap) ranks *= 2;
+    while (ranks < kSelectCluster && 2 * ranks * units <= 4 * 148 && (int64_t)ranks * kSelectSlice < s.cap) ranks *= 2;
     if (units * ranks > INT32_MAX || s.hkv > 65535) return WC_ERR_UNSUPPORTED;
     const int per = ((s.cap + ranks - 1) / ranks + 31) / 32 * 32;
     const int held = per < kSelectHeld ? per : kSelectHeld;
@@ -603,7 +613,9 @@ wc_status launch_evict(const EvictArgs& a, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, cache_select_kernel, a, held) != cudaSuccess) return WC_ERR_CUDA;
+    auto select = ranks == 1 ? cache_select_kernel<1> : ranks == 2 ? cache_select_kernel<2>
+                : ranks == 4 ? cache_select_kernel<4> : cache_select_kernel<8>;
+    if (cudaLaunchKernelEx(&cfg, select, a, held) != cudaSuccess) return WC_ERR_CUDA;
     const int slices = (s.d * s.esize + kMoveSlice - 1) / kMoveSlice + (s.dv * s.esize + kMoveSlice - 1) / kMoveSlice;
     const int rows = kMoveThreads / 32 * kCopyRows;
     cfg.gridDim = dim3(1 + (a.into ? (a.keep + rows - 1) / rows : slices), s.hkv, s.B);
