@@ -57,41 +57,23 @@ __device__ __forceinline__ float2 halves(uint64_t p) {
     return v;
 }
 
-template <typename T> __device__ __forceinline__ void load_chunk(const char* p, uint64_t* x);
-template <> __device__ __forceinline__ void load_chunk<float>(const char* p, uint64_t* x) {
-    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
-    x[0] = v.x;
-    x[1] = v.y;
-}
-template <> __device__ __forceinline__ void load_chunk<__nv_bfloat16>(const char* p, uint64_t* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = pair_of(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
-}
-
-// Logits of NT staged keys against RG query rows: lane = (key, part of d).
+// Logits of NT staged fp32 keys against RG query rows: lane = (key, part of d).
 // Every lane ends with its key's whole sums.
-template <typename T, int RG, int NT>
+template <int RG, int NT>
 __device__ __forceinline__ void tile_logits(const char* krows, int k_row, const float* q, int d, float s[RG]) {
-    constexpr int kPer = 16 / sizeof(T);
     const int lane = threadIdx.x & 31, key = lane % NT, part = lane / NT;
     const char* row = krows + key * k_row;
     uint64_t sum[RG];
 #pragma unroll
     for (int g = 0; g < RG; ++g) sum[g] = 0;
 #pragma unroll 4
-    for (int c = part; c < d / kPer; c += 32 / NT) {
-        uint64_t x[kPer / 2];
-        load_chunk<T>(row + c * 16, x);
+    for (int c = part; c < d / 4; c += 32 / NT) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(row + c * 16);
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
-#pragma unroll
-            for (int i = 0; i < kPer; i += 4) {
-                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(q + g * d + c * kPer + i);
-                sum[g] = fma2(x[i / 2], y.x, sum[g]);
-                sum[g] = fma2(x[i / 2 + 1], y.y, sum[g]);
-            }
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(q + g * d + c * 4);
+            sum[g] = fma2(x.x, y.x, sum[g]);
+            sum[g] = fma2(x.y, y.y, sum[g]);
         }
     }
 #pragma unroll
@@ -308,33 +290,120 @@ __device__ __forceinline__ void join_warps(const AttendArgs& a, const float* mer
     }
 }
 
-// Query rows of one unit into shared memory as fp32, scaled to log2 units;
+// fp32 query rows of one unit into shared memory, scaled to log2 units;
 // rows past the group are zero.
-template <typename T, int RG, int WARPS>
+template <int RG, int WARPS>
 __device__ __forceinline__ void load_queries(const AttendArgs& a, int b, int g0, int rows, float* q) {
-    const T* src = static_cast<const T*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
+    const float* src = static_cast<const float*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
     for (int i = threadIdx.x; i < RG * a.s.d; i += WARPS * 32) {
         const int g = i / a.s.d, c = i - g * a.s.d;
-        q[i] = g < rows ? to_f32(src[g * a.q_head + c]) * a.qscale : 0.f;
+        q[i] = g < rows ? src[g * a.q_head + c] * a.qscale : 0.f;
     }
 }
 
+// ---------------------------------------------------------------- tensor cores
+
+__device__ __forceinline__ void ldmatrix4(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// a b, 16 x 8 x 16, bf16 in, fp32 sums.
+__device__ __forceinline__ void mma16816_new(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// c += a b.
+__device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The three bf16 terms of a pair of weights, x = t0 + t1 + t2 up to 2^-24 x:
+// one term alone (half a step, 2^-9 relative) would be the largest error of the
+// whole attention, whose output is fp32.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t t[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        t[i] = pack_bf16(x, y);
+        x -= __uint_as_float(t[i] << 16);
+        y -= __uint_as_float(t[i] & 0xffff0000u);
+    }
+}
+
+// The bf16 query fragments of one unit for 16-row tiles: rows quad and, where
+// kRows = 16, quad + 8; with fewer rows, row quad % kRows (rows past the group
+// are zeros).
+template <int DP, int kRows>
+struct QueryFragments {
+    static constexpr int kRegs = kRows == 16 ? 4 : 2;
+    uint32_t q[DP / 16][kRegs];
+    __device__ __forceinline__ void load(const AttendArgs& a, int b, int g0, int rows) {
+        const int lane = threadIdx.x & 31, quad = lane >> 2, pair = lane & 3;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.Q) + b * a.q_batch + (int64_t)g0 * a.q_head;
+        auto two = [&](int row, int col) {
+            uint32_t v = 0;
+            if (row < rows && col < a.s.d) {
+                const __nv_bfloat16* p = src + row * a.q_head + col;
+                if (a.q_pairs) v = *reinterpret_cast<const uint32_t*>(p);
+                else v = (uint32_t)__bfloat16_as_ushort(p[0]) | (uint32_t)__bfloat16_as_ushort(p[1]) << 16;
+            }
+            return v;
+        };
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            const int col = k * 16 + pair * 2;
+            if (kRows == 16) {
+                q[k][0] = two(quad, col), q[k][1] = two(quad + 8, col);
+                q[k][kRegs - 2] = two(quad, col + 8), q[k][kRegs - 1] = two(quad + 8, col + 8);
+            } else {
+                q[k][0] = two(quad % kRows, col);
+                q[k][1] = two(quad % kRows, col + 8);
+            }
+        }
+    }
+    // x += the k-th 16 columns against 8 keys
+    __device__ __forceinline__ void step(float x[4], int k, uint32_t b0, uint32_t b1) const {
+        if (kRows == 16) mma16816(x, q[k][0], q[k][1], q[k][kRegs - 2], q[k][kRegs - 1], b0, b1);
+        else mma16816(x, q[k][0], q[k][0], q[k][1], q[k][1], b0, b1);
+    }
+};
+
+constexpr int kCoresetWarps = 4;
+
 // Shared memory of one coreset block, in bytes: two stages a warp of NT keys
 // and their rows of W (as they lie in memory, dv + 1 values each, and up to 12
-// bytes before them).  The warps' sums go where the stages were.
-template <int NT, int RG, int WARPS>
+// bytes before them).  The warps' sums go where the stages were.  The end
+// leaves room for a lane that reads its columns past dv (and drops them).
+template <typename T, int NT, int RG, int DP>
 struct CoresetSmem {
-    int k_row, w_row, w, stage, q, p, total;
-    __host__ __device__ CoresetSmem(int d, int dv, int esize) {
-        k_row = d * esize;
-        if ((k_row / 16) % 2 == 0) k_row += 16;
-        w_row = (dv + 1) * 4;
+    int k_row, w, stage, q, p, total;
+    __host__ __device__ CoresetSmem(int d, int dv) {
+        k_row = sizeof(T) == 2 ? DP * 2 + 16 : (d / 4 % 2 ? d * 4 : d * 4 + 16);   // an odd number of 16-byte units
         w = NT * k_row;
-        stage = (w + 12 + NT * w_row + 15) / 16 * 16;
-        const int stages = WARPS * 2 * stage, merge = WARPS * RG * (dv + 2) * 4;
+        stage = (w + 12 + NT * (dv + 1) * 4 + 15) / 16 * 16;
+        const int stages = kCoresetWarps * 2 * stage, merge = kCoresetWarps * RG * (dv + 2) * 4;
         q = ((stages > merge ? stages : merge) + 15) / 16 * 16;
-        p = q + RG * d * 4;
-        total = p + WARPS * NT * RG * 8;
+        p = q + (sizeof(T) == 2 ? 0 : RG * d * 4);
+        total = p + kCoresetWarps * NT * RG * 8 + 512;
     }
 };
 
@@ -348,18 +417,20 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // by side, so the 16-byte pieces that hold them are copied (4-byte copies took
 // 1.3 times as long over all), the last few values one by one.  A lane holds
 // columns lane, lane + 32, ... and the row's last value is its weight in the
-// normaliser.  Sums in fp32 on CUDA cores: W's values cancel one another.
-constexpr int kCoresetWarps = 4;
-
-template <typename T, int RG, int NT, int COLS>
+// normaliser.  The logits of bf16 keys on tensor cores, the sums in fp32 on
+// CUDA cores: W's values cancel one another.  Bound by the issue of those sums
+// and of the copies (8 x 1024 rows of 8 heads in about 14 us, 3.5 TB/s).
+template <typename T, int RG, int NT, int DP>
 __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const AttendArgs a) {
-    constexpr int WARPS = kCoresetWarps;
+    constexpr int WARPS = kCoresetWarps, COLS = DP / 32;
+    constexpr bool kTensor = sizeof(T) == 2;     // logits on tensor cores
+    static_assert(!kTensor || NT == 8, "a step is one column octet of the product");
     extern __shared__ __align__(128) char smem[];
     grid_dependency_wait();
     grid_dependents_launch();
     const View& s = a.s;
     const int index = blockIdx.x;
-    const CoresetSmem<NT, RG, WARPS> L(s.d, s.dv, sizeof(T));
+    const CoresetSmem<T, NT, RG, DP> L(s.d, s.dv);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* q = reinterpret_cast<float*>(smem + L.q);
     uint64_t* p = reinterpret_cast<uint64_t*>(smem + L.p) + warp * NT * RG;   // a step's weights, each twice
@@ -380,10 +451,11 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
         if (live > 0) {
             const uint32_t kd = (uint32_t)__cvta_generic_to_shared(stages + stage * L.stage), wd = kd + L.w;
             const char* k = static_cast<const char*>(a.Ks) + (base + at) * s.d * (int64_t)sizeof(T);
-            int row = lane / ck, c = lane - row * ck;
-            for (int i = lane; i < NT * ck; i += 32) {
-                if (row < live) cp_async16(kd + row * L.k_row + c * 16, k + i * 16);
-                for (c += 32; c >= ck; c -= ck) ++row;
+            constexpr int kChunks = DP * (int)sizeof(T) / 16;
+#pragma unroll
+            for (int i = 0; i < NT * kChunks; i += 32) {
+                const int row = (i + lane) / kChunks, c = (i + lane) % kChunks;
+                cp_async16_if(row < live && c < ck, kd + row * L.k_row + c * 16, k + (row * ck + c) * 16);
             }
             const int64_t w0 = (base + at) * (s.dv + 1), w1 = w0 + live * (s.dv + 1);   // values [w0, w1) of W
             const int pieces = (int)(w1 / 4 - w0 / 4);
@@ -392,54 +464,100 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
         }
         cp_async_commit();
     };
+    if (kTensor && s.d < DP) {   // columns past the width are never copied and count as zeros
+        for (int i = lane; i < L.stage / 8; i += 32) reinterpret_cast<uint4*>(stages)[i] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+    }
     int at = first + warp * NT;
     load(0, at);
-    load_queries<T, RG, WARPS>(a, b, h * s.group + rt * a.rows, rows, q);
+    const int g0 = h * s.group + rt * a.rows;
+    QueryFragments<kTensor ? DP : 16, kTensor ? RG : 4> qf;
+    if (kTensor) qf.load(a, b, g0, rows);
+    else load_queries<RG, WARPS>(a, b, g0, rows, q);
     __syncthreads();
-    float m[RG], l[RG];
+    constexpr int kRefs = !kTensor ? RG : RG == 16 ? 2 : 1;   // references a lane holds: of all rows, or of its own
+    float m[kRefs], l[RG];
+#pragma unroll
+    for (int r = 0; r < kRefs; ++r) m[r] = -CUDART_INF_F;
     uint64_t o[RG][COLS / 2];   // columns lane + 64 i and 32 further on
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
-        m[g] = -CUDART_INF_F;
         l[g] = 0.f;
 #pragma unroll
         for (int i = 0; i < COLS / 2; ++i) o[g][i] = 0;
     }
+    auto rescale = [&](int g, float f) {
+        l[g] *= f;
+#pragma unroll
+        for (int i = 0; i < COLS / 2; ++i) o[g][i] = mul2(o[g][i], pair_of(f, f));
+    };
     for (int stage = 0; at < last; at += WARPS * NT, stage ^= 1) {
         load(stage ^ 1, at + WARPS * NT);
         cp_async_wait<1>();
         __syncwarp();
         const char* krows = stages + stage * L.stage;
         const float* wrows = reinterpret_cast<const float*>(krows + L.w) + (int)(((base + at) * (s.dv + 1)) & 3);
-        float x[RG];
-        tile_logits<T, RG, NT>(krows, L.k_row, q, s.d, x);
-        const int key = lane % NT, live = min(NT, last - at);
+        const int live = min(NT, last - at);
+        if constexpr (kTensor) {
+            // a lane: keys 2 pair and 2 pair + 1 of row quad (and quad + 8)
+            const int quad = lane >> 2, pair = lane & 3;
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t kd = (uint32_t)__cvta_generic_to_shared(krows) + (lane & 7) * L.k_row + (lane >> 3) * 16;
 #pragma unroll
-        for (int g = 0; g < RG; ++g) {
-            const float v = key < live ? x[g] : -CUDART_INF_F;
-            float top = v;
-#pragma unroll
-            for (int e = 1; e < NT; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-            if (top > m[g]) {
-                const float f = ex2(m[g] - top);
-                m[g] = top;
-                l[g] *= f;
-#pragma unroll
-                for (int i = 0; i < COLS / 2; ++i) o[g][i] = mul2(o[g][i], pair_of(f, f));
+            for (int k = 0; k < DP / 32; ++k) {
+                uint32_t f[4];
+                ldmatrix4(f, kd + k * 64);
+                qf.step(x, 2 * k, f[0], f[1]);
+                qf.step(x, 2 * k + 1, f[2], f[3]);
             }
-            const float w = ex2(v - (m[g] == -CUDART_INF_F ? 0.f : m[g]));
-            if (lane < NT) p[key * RG + g] = pair_of(w, w);
+#pragma unroll
+            for (int r = 0; r < kRefs; ++r) {
+                float y[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) y[e] = pair * 2 + e < live ? x[2 * r + e] * a.qscale : -CUDART_INF_F;
+                float top = fmaxf(y[0], y[1]);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const bool grow = top > m[r] + 8.f;   // (the reference follows when the maximum has grown by 2^8)
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? ex2(m[r] - top) : 1.f;
+                    if (grow) m[r] = top;
+#pragma unroll
+                    for (int g = 0; g < (RG < 8 ? RG : 8); ++g) rescale((g + 8 * r) % RG, __shfl_sync(0xffffffffu, f, g * 4));
+                }
+                const float ref = m[r] == -CUDART_INF_F ? 0.f : m[r];
+                if (quad < RG)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float w = ex2(y[e] - ref);
+                        p[(pair * 2 + e) * RG + quad + 8 * r] = pair_of(w, w);
+                    }
+            }
+        } else {
+            float x[RG];
+            tile_logits<RG, NT>(krows, L.k_row, q, s.d, x);
+            const int key = lane % NT;
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                const float v = key < live ? x[g] : -CUDART_INF_F;
+                float top = v;
+#pragma unroll
+                for (int e = 1; e < NT; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+                if (top > m[g % kRefs]) {
+                    const float f = ex2(m[g % kRefs] - top);
+                    m[g % kRefs] = top;
+                    rescale(g, f);
+                }
+                const float w = ex2(v - (m[g % kRefs] == -CUDART_INF_F ? 0.f : m[g % kRefs]));
+                if (lane < NT) p[key * RG + g] = pair_of(w, w);
+            }
         }
         __syncwarp();
-#pragma unroll 4
-        for (int j = 0; j < live; ++j) {
+        auto add_row = [&](int j) {
             const float* w = wrows + j * (s.dv + 1);
             uint64_t y[COLS / 2];
 #pragma unroll
-            for (int i = 0; i < COLS / 2; ++i) {
-                const int c = lane + 64 * i;
-                y[i] = pair_of(c < s.dv ? w[c] : 0.f, c + 32 < s.dv ? w[c + 32] : 0.f);
-            }
+            for (int i = 0; i < COLS / 2; ++i) y[i] = pair_of(w[lane + 64 * i], w[lane + 64 * i + 32]);   // (past dv: dropped)
             const float z = w[s.dv];
 #pragma unroll
             for (int g = 0; g < RG; ++g) {
@@ -448,6 +566,13 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
 #pragma unroll
                 for (int i = 0; i < COLS / 2; ++i) o[g][i] = fma2(e, y[i], o[g][i]);
             }
+        };
+        if (live == NT) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) add_row(j);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < live; ++j) add_row(j);
         }
         __syncwarp();
     }
@@ -465,8 +590,8 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
             if (c < s.dv) row[c] = v.x;
             if (c + 32 < s.dv) row[c + 32] = v.y;
         }
-        if (lane == 0) {
-            row[s.dv] = m[g];
+        if (lane == (kTensor ? g % 8 * 4 : 0)) {   // (the lane that holds the row's reference)
+            row[s.dv] = m[kTensor ? g / 8 : g % kRefs];
             row[s.dv + 1] = l[g];
         }
     }
@@ -659,54 +784,6 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
     if (a.csplits) grid_dependency_wait();
 }
 
-// ---------------------------------------------------------------- tensor cores
-
-__device__ __forceinline__ void ldmatrix4(uint32_t r[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldmatrix4t(uint32_t r[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-// a b, 16 x 8 x 16, bf16 in, fp32 sums.
-__device__ __forceinline__ void mma16816_new(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                 "{%10,%10,%10,%10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-// c += a b.
-__device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                 "{%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
-// The three bf16 terms of a pair of weights, x = t0 + t1 + t2 up to 2^-24 x:
-// one term alone (half a step, 2^-9 relative) would be the largest error of the
-// whole attention, whose output is fp32.
-__device__ __forceinline__ void split_bf16(float x, float y, uint32_t t[3]) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        t[i] = pack_bf16(x, y);
-        x -= __uint_as_float(t[i] << 16);
-        y -= __uint_as_float(t[i] & 0xffff0000u);
-    }
-}
-
 constexpr int kMmaKeys = 16;     // keys of one warp's step
 // Stages of a warp's ring, and warps of a block: what fits two blocks an SM (one for the widest rows).
 template <int DP> constexpr int kMmaStages = DP > 128 ? 2 : 3;
@@ -768,33 +845,8 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         const int rows = min(a.rows, s.group - now.rt * a.rows), g0 = now.h * s.group + now.rt * a.rows;
         const int start = now.k, last = min(now.tiles, now.k + now.left);
         const int64_t row0 = (int64_t)now.b * s.hq + g0, part_row = now.part_row(a);
-        // Query fragments, as they are (the logits are scaled in fp32): rows
-        // quad and, where the rows are not copies, quad + 8.
-        uint32_t q[DP / 16][SETS == 3 ? 4 : 2];
-        {
-            const bf16* src = static_cast<const bf16*>(a.Q) + now.b * a.q_batch + (int64_t)g0 * a.q_head;
-            auto two = [&](int row, int col) {
-                uint32_t v = 0;
-                if (row < rows && col < s.d) {
-                    const bf16* p = src + row * a.q_head + col;
-                    if (a.q_pairs) v = *reinterpret_cast<const uint32_t*>(p);
-                    else v = (uint32_t)__bfloat16_as_ushort(p[0]) | (uint32_t)__bfloat16_as_ushort(p[1]) << 16;
-                }
-                return v;
-            };
-            const int r0 = quad % kRows;
-#pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                const int col = k * 16 + pair * 2;
-                if (SETS == 3) {
-                    q[k][0] = two(quad, col); q[k][1] = two(quad + 8, col);
-                    q[k][SETS == 3 ? 2 : 0] = two(quad, col + 8); q[k][SETS == 3 ? 3 : 1] = two(quad + 8, col + 8);
-                } else {
-                    q[k][0] = two(r0, col);
-                    q[k][1] = two(r0, col + 8);
-                }
-            }
-        }
+        QueryFragments<DP, kRows> q;                       // (as they are: the logits are scaled in fp32)
+        q.load(a, now.b, g0, rows);
         uint64_t o[DP / 8][2];                             // pairs of fp32 sums: row quad, row quad + 8
         float m[kMine], l[kMine];
 #pragma unroll
@@ -820,13 +872,8 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
             for (int k = 0; k < DP / 16; ++k) {
                 uint32_t f[4];
                 ldmatrix4(f, base + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
-                if (SETS == 3) {
-                    mma16816(x[0], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[0], f[1]);
-                    mma16816(x[1], q[k][0], q[k][1], q[k][SETS == 3 ? 2 : 0], q[k][SETS == 3 ? 3 : 1], f[2], f[3]);
-                } else {
-                    mma16816(x[0], q[k][0], q[k][0], q[k][1], q[k][1], f[0], f[1]);
-                    mma16816(x[1], q[k][0], q[k][0], q[k][1], q[k][1], f[2], f[3]);
-                }
+                q.step(x[0], k, f[0], f[1]);
+                q.step(x[1], k, f[2], f[3]);
             }
         }
         uint32_t w[kMine][2][3];                           // weights' terms: [row][key octet][term]
@@ -1264,7 +1311,7 @@ wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel 
 template <int DP, int RG>
 wc_status run_simt(const AttendArgs& a, cudaStream_t st) {
     return run(a, cache_attend_simt_kernel<DP, RG>, kSimtWarps, SimtSmem<DP, RG>::total, kSimtKeys,
-               cache_coreset_kernel<float, RG, 8, DP / 32>, CoresetSmem<8, RG, kCoresetWarps>(a.s.d, a.s.dv, 4).total, st);
+               cache_coreset_kernel<float, RG, 8, DP>, CoresetSmem<float, 8, RG, DP>(a.s.d, a.s.dv).total, st);
 }
 
 template <int DP>
@@ -1280,10 +1327,9 @@ wc_status by_rows(const AttendArgs& a, cudaStream_t st) {
 template <int DP, int SETS>
 wc_status run_mma(const AttendArgs& a, cudaStream_t st) {
     constexpr int rows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
-    constexpr int keys = 8;   // (with 16, half as many warps an SM: 1.2 times as long)
     return run(a, cache_attend_mma_kernel<DP, SETS>, kMmaWarps<DP>, kMmaWarps<DP> * MmaRing<DP>::kBytes, kMmaKeys,
-               cache_coreset_kernel<__nv_bfloat16, rows, keys, DP / 32>,
-               CoresetSmem<keys, rows, kCoresetWarps>(a.s.d, a.s.dv, 2).total, st);
+               cache_coreset_kernel<__nv_bfloat16, rows, 8, DP>,
+               CoresetSmem<__nv_bfloat16, 8, rows, DP>(a.s.d, a.s.dv).total, st);
 }
 
 template <int DP>

@@ -476,12 +476,13 @@ class PagedCache:
         if code != 0:
             raise WildcatError(code, what)
 
-    def _empty(self, shape, dtype, stream):
-        """An output, allocated for the stream that writes it."""
+    def _empty(self, shape, strides, dtype, stream):
+        """An output, allocated for the stream that writes it (the strides are
+        those of a contiguous tensor; given, they spare a microsecond)."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty_strided(shape, strides, dtype=dtype, device=self.device)
 
     # ---- calls
 
@@ -523,10 +524,10 @@ class PagedCache:
             if rank is not None:
                 self._tensor(rank, "rank", (self.batch, self.hkv), torch.int32)
         if out is None:
-            out = self._empty(self._o_shape, torch.float32, stream)
+            out = self._empty(self._o_shape, (self.hq * self.dv, self.dv, 1), torch.float32, stream)
         else:
             self._tensor(out, "out", self._o_shape, torch.float32)
-        lse = self._empty((self.batch, self.hq), torch.float32, stream) if return_lse else None
+        lse = self._empty((self.batch, self.hq), (self.hq, 1), torch.float32, stream) if return_lse else None
         sq = Q.stride()
         self._launch(self._attend, "wc_cache_attend", stream,
                      (self._shape_ref, Q.data_ptr(), sq[0], sq[1], *self._pools, lens.data_ptr(), r,
@@ -557,9 +558,9 @@ class PagedCache:
         keep, sink, recent = int(keep), int(sink), int(recent)
         if not (1 <= keep <= self.cap and sink >= 0 and recent >= 0 and sink + recent <= keep):
             raise WildcatError(1, "PagedCache.evict: 1 <= keep <= capacity, sink + recent <= keep")
-        idx = self._empty((self.batch, self.hkv, keep), torch.int32, stream)
+        idx = self._empty((self.batch, self.hkv, keep), (self.hkv * keep, keep, 1), torch.int32, stream)
         if lens_out is None:
-            lens_out = self._empty(self._seqs, torch.int32, stream)
+            lens_out = self._empty(self._seqs, (1,), torch.int32, stream)
         else:
             self._tensor(lens_out, "lens_out", self._seqs, torch.int32)
         self._launch(self._evict, "wc_cache_evict", stream,
