@@ -231,7 +231,8 @@ constexpr int kSelectBins = 2048 / kSelectThreads;   // of a thread
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectCluster = 8;             // blocks that may share one (sequence, kv head)
 constexpr int kSelectSlice = 4096;            // positions of a block before another one joins it
-constexpr int kSelectHeld = 40960;            // keys a block holds in shared memory, at most
+constexpr int kSelectHeld = 40960;            // keys a block holds in shared memory, at most,
+constexpr int kSelectHeldMany = 12288;        // and where there are more blocks than SMs (three an SM then)
 
 // References to the pages of sequence b: one for each page its tokens use, one
 // for each page of `into` that it will write.  The counts start at 0: of two
@@ -599,7 +600,7 @@ wc_status launch_evict(const EvictArgs& a, cudaStream_t st) {
     while (ranks < kSelectCluster && 2 * ranks * units <= 4 * 148 && (int64_t)ranks * kSelectSlice < s.cap) ranks *= 2;
     if (units * ranks > INT32_MAX || s.hkv > 65535) return WC_ERR_UNSUPPORTED;
     const int per = ((s.cap + ranks - 1) / ranks + 31) / 32 * 32;
-    const int held = per < kSelectHeld ? per : kSelectHeld;
+    const int most = units * ranks > 148 ? kSelectHeldMany : kSelectHeld, held = per < most ? per : most;
     cudaLaunchAttribute at[2]{};
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

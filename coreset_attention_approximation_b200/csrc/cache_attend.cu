@@ -1033,7 +1033,8 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
 // sets' weights 2^(m - M) into shared memory, a set a thread, then the sums,
 // four columns a thread and the sets spread over the rest (there are up to
 // hundreds of sets and few rows, and what counts is the loads in flight).  With
-// scores, the others take kScoreKeys positions of one (sequence, kv head) each:
+// scores, the others (`chunks` for each sequence and kv head, which bounds them where
+// the tables are far larger than the lengths) take kScoreKeys positions at a time:
 // the rows' references and normalisers first (a warp a row), then the logits
 // that the pages' kernel left, 2^(x - m) / L summed over the group's rows.
 constexpr int kJoinThreads = 256;
@@ -1042,7 +1043,7 @@ constexpr int kJoinSets = 1024;   // sets whose weights are held at a time
 constexpr int kScoreKeys = 2048;
 constexpr int kScoreRows = 64;    // rows whose references are held at a time
 
-__global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const AttendArgs a, int tile, int warps, int cols) {
+__global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const AttendArgs a, int tile, int warps, int cols, int chunks) {
     __shared__ int place_sh[1 + kJoinWarps];
     __shared__ __align__(16) float4 sums[kJoinThreads];
     __shared__ float weight[kJoinSets];
@@ -1054,7 +1055,6 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
     const int per_seq = cols ? s.hq * ((dv + cols - 1) / cols) : (s.hq + kJoinWarps - 1) / kJoinWarps;
     const int row_blocks = s.B * per_seq;
     const bool score = (int)blockIdx.x >= row_blocks;
-    const int chunks = (s.cap + kScoreKeys - 1) / kScoreKeys;
     int b, hq0, key0 = 0, col0 = 0;
     if (!score) {
         b = blockIdx.x / per_seq;
@@ -1069,6 +1069,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
     }
     const int len = checked_len(a.lens, b, s.cap, a.status);
     if (score && key0 >= len) return;
+    const int key_first = key0;
     const Place at = scan_tiles<kJoinThreads>(s, a.lens, tile, per_tile, b, nullptr, 1, a.status, place_sh);
     const Share share(at.total, warps);
     const int tiles = (len + tile - 1) / tile;
@@ -1202,38 +1203,43 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
         if (threadIdx.x == 0 && col0 == 0 && a.lse) a.lse[row] = log_sum(m, l);
         return;
     }
-    float acc[kScoreKeys / kJoinThreads];
+    // the stretches of kScoreKeys positions that this block takes, every chunks-th of them
+    for (; key0 < len; key0 += chunks * kScoreKeys) {
+        float acc[kScoreKeys / kJoinThreads];
 #pragma unroll
-    for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) acc[i] = 0.f;
-    for (int r0 = 0; r0 < s.group; r0 += kScoreRows) {
-        const int rows = min(kScoreRows, s.group - r0);
-        __syncthreads();
-        for (int r = warp; r < rows; r += kJoinWarps) {
-            find_sets(hq0 + r0 + r);
-            float m, l;
-            totals(m, l);
-            if (lane == 0) {
-                refs[r][0] = m == -CUDART_INF_F ? 0.f : m;
-                refs[r][1] = nothing(m, l) ? 0.f : 1.f / l;   // no weight anywhere: 0 for every key
+        for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) acc[i] = 0.f;
+        for (int r0 = 0; r0 < s.group; r0 += kScoreRows) {
+            const int rows = min(kScoreRows, s.group - r0);
+            if (key0 == key_first || s.group > kScoreRows) {
+                __syncthreads();
+                for (int r = warp; r < rows; r += kJoinWarps) {
+                    find_sets(hq0 + r0 + r);
+                    float m, l;
+                    totals(m, l);
+                    if (lane == 0) {
+                        refs[r][0] = m == -CUDART_INF_F ? 0.f : m;
+                        refs[r][1] = nothing(m, l) ? 0.f : 1.f / l;   // no weight anywhere: 0 for every key
+                    }
+                }
+                __syncthreads();
             }
-        }
-        __syncthreads();
 #pragma unroll 4
-        for (int r = 0; r < rows; ++r) {
-            const float* x = a.logits + ((int64_t)b * s.hq + hq0 + r0 + r) * s.cap;
-            const float ref = refs[r][0], inv = refs[r][1];
+            for (int r = 0; r < rows; ++r) {
+                const float* x = a.logits + ((int64_t)b * s.hq + hq0 + r0 + r) * s.cap;
+                const float ref = refs[r][0], inv = refs[r][1];
 #pragma unroll
-            for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) {
-                const int key = key0 + i * kJoinThreads + threadIdx.x;
-                if (key < len) acc[i] = fmaf(ex2(x[key] - ref), inv, acc[i]);
+                for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) {
+                    const int key = key0 + i * kJoinThreads + threadIdx.x;
+                    if (key < len) acc[i] = fmaf(ex2(x[key] - ref), inv, acc[i]);
+                }
             }
         }
-    }
-    float* out = a.scores + ((int64_t)b * s.hkv + hq0 / s.group) * s.cap;
+        float* out = a.scores + ((int64_t)b * s.hkv + hq0 / s.group) * s.cap;
 #pragma unroll
-    for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) {
-        const int key = key0 + i * kJoinThreads + threadIdx.x;
-        if (key < len) out[key] += acc[i];
+        for (int i = 0; i < kScoreKeys / kJoinThreads; ++i) {
+            const int key = key0 + i * kJoinThreads + threadIdx.x;
+            if (key < len) out[key] += acc[i];
+        }
     }
 }
 
@@ -1285,7 +1291,9 @@ wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel 
     int room = 0, core_room = 0;
     if (resident_blocks(reinterpret_cast<const void*>(pages), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
     const int64_t units = (int64_t)a.s.B * a.s.hkv * a.row_tiles, most = units * ((a.s.cap + tile - 1) / tile);
-    const int64_t chunks = (a.s.cap + kScoreKeys - 1) / kScoreKeys, rows = (int64_t)a.s.B * a.s.hq;
+    const int64_t rows = (int64_t)a.s.B * a.s.hq, pairs = (int64_t)a.s.B * a.s.hkv;
+    // score blocks of one (sequence, kv head): a stretch each, at most about 4096 blocks in all
+    const int64_t chunks = min((int64_t)(a.s.cap + kScoreKeys - 1) / kScoreKeys, (4096 + pairs - 1) / pairs);
     // Where the rows are at most the blocks that the GPU holds at once, a block for as few columns (32 and up) of
     // a row as that allows (32 rows of 150 sets each: 3 us against 8 for a warp a row); where they are more, a
     // warp for a row (1024 rows of 5 sets: 7 us against 9).
@@ -1293,7 +1301,7 @@ wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel 
     int cols = rows <= most_blocks ? 32 : 0;
     while (cols && cols < a.s.dv && rows * ((a.s.dv + cols - 1) / cols) > most_blocks) cols *= 2;
     const int64_t join = (cols ? rows * ((a.s.dv + cols - 1) / cols) : (int64_t)a.s.B * ((a.s.hq + kJoinWarps - 1) / kJoinWarps)) +
-                         (a.scores ? chunks * a.s.B * a.s.hkv : 0);
+                         (a.scores ? chunks * pairs : 0);
     if (most > INT32_MAX || join > INT32_MAX) return WC_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
     if (a.csplits) {
         if (units * a.csplits > INT32_MAX) return WC_ERR_UNSUPPORTED;
@@ -1303,7 +1311,7 @@ wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel 
     }
     a.blocks = (int)min((most + warps - 1) / warps, (int64_t)min(room, max_warps(a.s) / warps));
     if (!launch(pages, a.blocks, warps * 32, smem, st, a) ||
-        !launch(cache_join_kernel, join, kJoinThreads, 0, st, a, tile, a.blocks * warps, cols))
+        !launch(cache_join_kernel, join, kJoinThreads, 0, st, a, tile, a.blocks * warps, cols, (int)chunks))
         return WC_ERR_CUDA;
     return WC_OK;
 }

@@ -77,6 +77,8 @@ SHAPES = [
     (F32, 16, 1, 256, 256, 32, False),
     (F32, 6, 2, 8, 8, 5, True),
     (F32, 20, 2, 40, 136, 16, False),
+    (BF, 80, 1, 64, 64, 16, False),
+    (F32, 70, 1, 16, 16, 16, False),
 ]
 
 
@@ -104,6 +106,28 @@ def test_attend_thousands_of_sequences(dtype):
     lens = [(7 * i) % 23 if i % 5 else 0 for i in range(2500)] + [90] + [0] * 30
     case = Case(dtype, len(lens), 2, 1, 16, 16, 8, 12, lens, seed=24)
     check_attend(case)
+
+
+def test_attend_in_tables_far_longer_than_the_sequences():
+    """Room for 2^20 tokens, some of it used: positions beyond what one round
+    of the score blocks takes, and none of it elsewhere."""
+    page, n = 4096, 90000
+    case = Case(BF, 1, 2, 1, 16, 16, page, 22, [n], seed=27)
+    k, v, table, q, lens, _ = case.on_gpu()
+    wide = torch.full((600, 256), -1, dtype=torch.int32)
+    wide[7, :22] = case.table[0]
+    q600 = torch.zeros(600, 2, 16, dtype=BF, device="cuda")
+    q600[7] = q[0]
+    l600 = torch.zeros(600, dtype=torch.int32, device="cuda")
+    l600[7] = n
+    cache = wildcat.PagedCache(k, v, wide.cuda(), hq=2, scores=torch.zeros(600, 1, 256 * page, device="cuda"))
+    out = cache.attend(q600, l600, accumulate=True)
+    assert cache.check() == 0
+    want, _, wts, bound = cache_ref.attend(case)
+    assert float((out[7].cpu().double() - want[0]).abs().max()) <= bound * 6
+    assert float((cache.scores[7, 0, :n].cpu().double() - wts[0, 0, :n]).abs().max()) <= 2 * bound
+    cache.scores[7, 0, :n] = 0
+    assert not cache.scores.any() and not out[:7].any() and not out[8:].any()
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -154,7 +178,9 @@ def coreset_of(case, r, seed, full_rank=True):
 
 @pytest.mark.parametrize("dtype,hq,hkv,d,dv,r", [(BF, 32, 8, 128, 128, 200), (BF, 4, 4, 64, 64, 1),
                                                  (BF, 12, 1, 96, 40, 65), (F32, 8, 2, 64, 64, 300),
-                                                 (F32, 16, 1, 256, 256, 33), (BF, 2, 1, 256, 256, 1000)])
+                                                 (F32, 16, 1, 256, 256, 33), (BF, 2, 1, 256, 256, 1000),
+                                                 (BF, 36, 1, 64, 64, 70), (F32, 20, 1, 40, 8, 9), (BF, 4, 2, 256, 8, 33),
+                                                 (F32, 2, 2, 8, 136, 12), (BF, 16, 2, 8, 256, 130)])
 @pytest.mark.parametrize("full", [True, False])
 def test_attend_with_a_coreset(dtype, hq, hkv, d, dv, r, full):
     """One softmax over the coreset and the pages; sequences without tokens
@@ -381,6 +407,26 @@ def test_evict_long(n):
     case.scores[0, 0] = torch.exp(3 * torch.randn(case.cap))
     case.scores[0, 1, 100:] = 0.0
     check_evict(case, 9000, 4, 500, False, False)
+
+
+def test_evict_more_than_is_held():
+    """Stretches of positions that a block cannot hold: many (sequence, kv
+    head) pairs, one of them long."""
+    g = torch.Generator().manual_seed(28)
+    B, n, page, keep = 200, 30000, 1000, 700
+    table = torch.full((B, 31), -1, dtype=torch.int32)
+    table[3, :30] = torch.randperm(31, generator=g)[:30].to(torch.int32)
+    k = torch.randn(31, 1, page, 8, generator=g).to(BF).cuda()
+    scores = torch.rand(B, 1, 31 * page, generator=g)
+    scores[3, 0, ::3] = 0.75
+    lens = torch.zeros(B, dtype=torch.int32)
+    lens[3] = n
+    cache = wildcat.PagedCache(k, k.clone(), table.cuda(), hq=1, scores=scores.cuda())
+    res = cache.evict(lens.cuda(), keep, sink=5, recent=50)
+    assert cache.check() == 0
+    want = cache_ref.kept_positions(scores[3, 0].numpy(), n, keep, 5, 50)
+    assert np.array_equal(res["idx"][3, 0].cpu().numpy(), want)
+    assert int(res["lens"][3]) == keep and int(res["lens"].sum()) == keep
 
 
 def test_evict_again_and_again():
