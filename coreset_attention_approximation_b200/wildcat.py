@@ -418,7 +418,8 @@ class PagedCache:
             raise WildcatError(1, "PagedCache: sizes or strides")
         if self.device.type != "cuda":
             raise WildcatError(1, "PagedCache: the pages are on a GPU")
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        self.ws[: 256 + 8 * n_pages].zero_()     # the status word and the page counts; the rest is written first
         # what every call passes on, looked up once (a decode step's kernels are as short as the calls that launch them)
         self._shape_ref = ctypes.byref(self.shape)
         self._pools = (k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr())

@@ -282,9 +282,10 @@ wc_status wc_attend_noalloc(const wc_shape* shape, const void* Q, const void* Ks
  *   - scores [B, Hkv, cap] fp32: attention weight accumulated by position.
  *     They belong to a sequence, not to a page.
  *   - The workspace is the cache calls' own (wc_cache_workspace_bytes),
- *     256-byte aligned, zeroed before the first call and then used for one
- *     wc_cache only (evict keeps counts in it from call to call).  Calls that
- *     may overlap (two streams, two graphs) need a workspace each.
+ *     256-byte aligned, its first 256 + 8 n_pages bytes zeroed before the first
+ *     call, and then used for one wc_cache only (evict keeps counts in it from
+ *     call to call).  Calls that may overlap (two streams, two graphs) need a
+ *     workspace each.
  */
 typedef struct {
     int32_t batch;      /* B sequences, 1..65535 */
