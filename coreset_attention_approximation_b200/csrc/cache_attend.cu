@@ -122,6 +122,18 @@ struct Walk {
         h = unit / a.row_tiles;
         rt = unit - h * a.row_tiles;
     }
+    // tiles first, first + n, ... of one unit (short caches: a block has a unit)
+    __device__ __forceinline__ void one(const AttendArgs& a, int unit, int first, int tile) {
+        stretch = 0;
+        const int pair = unit / a.row_tiles;
+        rt = unit - pair * a.row_tiles;
+        b = pair / a.s.hkv;
+        h = pair - b * a.s.hkv;
+        len = checked_len(a.lens, b, a.s.cap, a.status);
+        tiles = (len + tile - 1) / tile;
+        k = first;
+        left = tiles - first;
+    }
     // past n tiles of this unit, to the next unit behind its last one (true then)
     __device__ __forceinline__ bool skip(const AttendArgs& a, int n, int tile) {
         left -= n;
@@ -599,6 +611,50 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
     join_warps<RG, WARPS>(a, merge, index, rows);
 }
 
+// Short caches: joins the sums that a block's warps left in shared memory for
+// the one unit that the block has, writes the rows, and adds the step's weights
+// to the scores.  lm: (normaliser, reference) by warp and row; there[w]: warp w
+// had tiles; piece(w, g, c): four of its sums.
+template <int WARPS, int ROWS, typename Piece>
+__device__ void finish_unit(const AttendArgs& a, const Walk& u, int64_t row0, int rows, const float2 (*lm)[ROWS],
+                            const int* there, float2* refs, Piece piece) {
+    const View& s = a.s;
+    const int c4 = s.dv / 4;
+    for (int i = threadIdx.x; i < rows * c4; i += WARPS * 32) {
+        const int g = i / c4, c = i - g * c4;
+        float m = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            if (there[w]) m = fmaxf(m, lm[w][g].y);
+        const float ref = m == -CUDART_INF_F ? 0.f : m;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            if (there[w]) {
+                const float f = ex2(lm[w][g].y - ref);
+                const float4 v = piece(w, g, c);
+                l = fmaf(f, lm[w][g].x, l);
+                o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+            }
+        const bool none = nothing(m, l);
+        float* to = a.out + (row0 + g) * s.dv + c * 4;
+        to[0] = none ? 0.f : o.x / l, to[1] = none ? 0.f : o.y / l;
+        to[2] = none ? 0.f : o.z / l, to[3] = none ? 0.f : o.w / l;
+        if (c == 0) {
+            if (a.lse) a.lse[row0 + g] = log_sum(m, l);
+            refs[g] = make_float2(ref, none ? 0.f : 1.f / l);
+        }
+    }
+    if (!a.logits) return;
+    __syncthreads();   // (also orders the block's own logits before their reading)
+    float* out = a.scores + ((int64_t)u.b * s.hkv + u.h) * s.cap;
+    for (int key = threadIdx.x; key < u.len; key += WARPS * 32) {
+        float sum = 0.f;
+        for (int g = 0; g < rows; ++g) sum = fmaf(ex2(a.logits[(row0 + g) * s.cap + key] - refs[g].x), refs[g].y, sum);
+        out[key] += sum;
+    }
+}
+
 // fp32 pages, on CUDA cores (their products keep 24 bits): 8 keys a step, two or
 // three stages a warp.  For the logits a lane holds one key and a quarter of the
 // width, for the values four columns (and, where fewer than 32 lanes cover the
@@ -613,14 +669,18 @@ struct SimtSmem {
     static constexpr int total = kSimtWarps * warp;
 };
 
-template <int DP, int RG>
+// SHORT: a block has one unit, its warps the unit's tiles in turn, and no join follows.
+template <int DP, int RG, bool SHORT>
 __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(const AttendArgs a) {
     constexpr int KEYS = kSimtKeys, kChunks = DP / 4;
     constexpr int kGroups = kChunks < 32 ? 32 / kChunks : 1;      // key groups of the value sums
     constexpr int kCols = kChunks < 32 ? 1 : kChunks / 32;        // a lane's column quadruples
     using L = SimtSmem<DP, RG>;
     extern __shared__ __align__(128) char smem[];
-    __shared__ int place_sh[1 + kSimtWarps], pre[kPlaces];
+    __shared__ int place_sh[1 + kSimtWarps], pre[SHORT ? 1 : kPlaces];
+    __shared__ float2 lm_sh[kSimtWarps][RG], refs[RG];
+    __shared__ int there[kSimtWarps];
+    constexpr int kStride = SHORT ? kSimtWarps : 1;
     if (!a.csplits) grid_dependency_wait();   // (with a coreset its kernel has waited)
     grid_dependents_launch();
     const View& s = a.s;
@@ -628,12 +688,16 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
     char* mem = smem + warp * L::warp;
     float* q = reinterpret_cast<float*>(mem + L::q);
     uint64_t* p = reinterpret_cast<uint64_t*>(mem + L::p);   // a step's weights, each twice (as a pair)
-    const int step = (s.B + kPlaces - 1) / kPlaces;
-    const Place at = scan_tiles<kSimtWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, -1, pre, step,
-                                                  a.status, place_sh);
-    const Share share(at.total, a.blocks * kSimtWarps);
     Walk now, ahead;
-    now.start(a, share, pre, step, blockIdx.x * kSimtWarps + warp, KEYS);
+    if (SHORT) {
+        now.one(a, blockIdx.x, warp, KEYS);
+        if (lane == 0) there[warp] = now.left > 0;
+    } else {
+        const int step = (s.B + kPlaces - 1) / kPlaces;
+        const Place at = scan_tiles<kSimtWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, -1, pre, step, a.status, place_sh);
+        now.start(a, Share(at.total, a.blocks * kSimtWarps), pre, step, blockIdx.x * kSimtWarps + warp, KEYS);
+    }
+    const Walk unit = now;
     ahead = now;
     SimtRing<DP> ring;
     ring.init(a, mem);
@@ -643,7 +707,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
         masks >>= 8;
         if (ahead.left > 0) {
             masks |= ring.fetch(a, stage) << (8 * (kStages - 1));
-            if (ahead.skip(a, 1, KEYS)) ring.enter(a, ahead);
+            if (ahead.skip(a, kStride, KEYS)) ring.enter(a, ahead);
             ring.locate(a, ahead);
         }
         cp_async_commit();
@@ -674,7 +738,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
 #pragma unroll
             for (int i = 0; i < kCols * 2; ++i) o[g][i] = 0;
         }
-        for (int at_k = start; at_k < last; ++at_k) {
+        for (int at_k = start; at_k < last; at_k += kStride) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
         fetch(stage == 0 ? kStages - 1 : stage - 1);   // the stage that the last step read is free
@@ -749,7 +813,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
         stage = stage + 1 == kStages ? 0 : stage + 1;
         }
         // finished rows where the share is the whole unit, else partial rows
-        const bool whole = start == 0 && last == now.tiles && !a.csplits && !a.logits;
+        const bool whole = !SHORT && start == 0 && last == now.tiles && !a.csplits && !a.logits;
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
 #pragma unroll
@@ -766,7 +830,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
                 for (int i = 0; i < kCols * 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], e);
             if (g >= rows) continue;
             const bool none = nothing(m[g], l[g]);
-            float* to = whole ? a.out + (row0 + g) * s.dv : a.parts + (part_row + g) * s.dv;
+            float* to = SHORT ? reinterpret_cast<float*>(mem) + g * s.dv   // (the ring is idle)
+                      : whole ? a.out + (row0 + g) * s.dv : a.parts + (part_row + g) * s.dv;
 #pragma unroll
             for (int n = 0; n < kCols; ++n) {
                 const int col = (lane + n * 32) * 4;
@@ -775,11 +840,22 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
                     for (int e = 0; e < 4; ++e) to[col + e] = whole ? (none ? 0.f : v[n * 4 + e] / l[g]) : v[n * 4 + e];
             }
             if (lane == 0) {
-                if (!whole) a.parts_lm[part_row + g] = make_float2(l[g], m[g]);
+                if (SHORT) lm_sh[warp][g] = make_float2(l[g], m[g]);
+                else if (!whole) a.parts_lm[part_row + g] = make_float2(l[g], m[g]);
                 else if (a.lse) a.lse[row0 + g] = log_sum(m[g], l[g]);
             }
         }
+        if (SHORT) break;
         now.skip(a, last - start, KEYS);
+    }
+    if (SHORT) {
+        __syncthreads();
+        const int g0 = unit.h * s.group + unit.rt * a.rows;
+        finish_unit<kSimtWarps, RG>(a, unit, (int64_t)unit.b * s.hq + g0, min(a.rows, s.group - unit.rt * a.rows), lm_sh,
+                                    there, refs, [&](int w, int g, int c) {
+                                        return *reinterpret_cast<const float4*>(smem + w * L::warp + (g * s.dv + c * 4) * 4);
+                                    });
+        return;
     }
     if (a.csplits) grid_dependency_wait();
 }
@@ -788,6 +864,12 @@ constexpr int kMmaKeys = 16;     // keys of one warp's step
 // Stages of a warp's ring, and warps of a block: what fits two blocks an SM (one for the widest rows).
 template <int DP> constexpr int kMmaStages = DP > 128 ? 2 : 3;
 template <int DP> constexpr int kMmaWarps = DP > 128 ? 6 : 4;
+
+// Four columns of a warp's sums as they stand in shared memory (see the kernel's end).
+template <int DP>
+__device__ __forceinline__ float4 sums_at(const float* sums, int row, int c) {
+    return *reinterpret_cast<const float4*>(sums + row * DP + ((c / 2 ^ (row & 7)) * 4 + (c & 1) * 2) * 2);
+}
 
 template <int DP> using MmaRing = Ring<kMmaKeys, DP, 2, kMmaStages<DP>>;
 
@@ -800,7 +882,8 @@ template <int DP> using MmaRing = Ring<kMmaKeys, DP, 2, kMmaStages<DP>>;
 //      the copies carry the terms, so one product adds all three
 //   2  up to 8 rows, each twice: two products
 //   3  up to 16 rows: three products
-template <int DP, int SETS>
+// SHORT: as above.
+template <int DP, int SETS, bool SHORT>
 __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(const AttendArgs a) {
     using bf16 = __nv_bfloat16;
     constexpr int kRows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
@@ -808,18 +891,25 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
     constexpr int kStages = kMmaStages<DP>, kBlockWarps = kMmaWarps<DP>;
     constexpr int kMine = SETS == 3 ? 2 : 1;               // rows of a lane
     extern __shared__ __align__(128) char smem[];
-    __shared__ int place_sh[1 + kBlockWarps], pre[kPlaces];
+    __shared__ int place_sh[1 + kBlockWarps], pre[SHORT ? 1 : kPlaces];
+    __shared__ float2 lm_sh[kBlockWarps][kRows], refs[kRows];
+    __shared__ int there[kBlockWarps];   // SHORT: 0, or 1 + where in its ring a warp's sums are
+    constexpr int kStride = SHORT ? kBlockWarps : 1;
     if (!a.csplits) grid_dependency_wait();   // (with a coreset its kernel has waited)
     grid_dependents_launch();
     const View& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = lane >> 2, pair = lane & 3;           // fragment row and column pair
-    const int step = (s.B + kPlaces - 1) / kPlaces;
-    const Place at = scan_tiles<kBlockWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, -1, pre, step,
-                                                  a.status, place_sh);
-    const Share share(at.total, a.blocks * kBlockWarps);
     Walk now, ahead;
-    now.start(a, share, pre, step, blockIdx.x * kBlockWarps + warp, KEYS);
+    if (SHORT) {
+        now.one(a, blockIdx.x, warp, KEYS);
+        if (lane == 0) there[warp] = now.left > 0;
+    } else {
+        const int step = (s.B + kPlaces - 1) / kPlaces;
+        const Place at = scan_tiles<kBlockWarps * 32>(s, a.lens, KEYS, s.hkv * a.row_tiles, -1, pre, step, a.status, place_sh);
+        now.start(a, Share(at.total, a.blocks * kBlockWarps), pre, step, blockIdx.x * kBlockWarps + warp, KEYS);
+    }
+    const Walk unit = now;
     ahead = now;
     MmaRing<DP> ring;
     char* mem = smem + warp * MmaRing<DP>::kBytes;
@@ -830,7 +920,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         masks >>= 16;
         if (ahead.left > 0) {
             masks |= (uint64_t)ring.fetch(a, stage) << (16 * (kStages - 1));
-            if (ahead.skip(a, 1, KEYS)) ring.enter(a, ahead);
+            if (ahead.skip(a, kStride, KEYS)) ring.enter(a, ahead);
             ring.locate(a, ahead);
         }
         cp_async_commit();
@@ -853,7 +943,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = 0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) m[i] = -CUDART_INF_F, l[i] = 0.f;
-        for (int at_k = start; at_k < last; ++at_k) {
+        for (int at_k = start; at_k < last; at_k += kStride) {
         cp_async_wait<kStages - 2>();
         __syncwarp();
         const uint32_t kd = stages + stage * MmaRing<DP>::kStage, vd = kd + KEYS * kRow;
@@ -965,7 +1055,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
         __syncwarp();
         }
         // finished rows where the share is the whole unit, else partial rows
-        const bool whole = start == 0 && last == now.tiles && !a.csplits && !a.logits;
+        const bool whole = !SHORT && start == 0 && last == now.tiles && !a.csplits && !a.logits;
         // The sums go through the stage that was read last (free until the next fetch): pairs of columns at
         // row quad (quad + 8), XOR-swizzled, then out in 16-byte pieces.  Straight from the fragments the
         // code is five times as long, and a warp that runs it once waits for its instructions.
@@ -982,9 +1072,14 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             const int g = quad + 8 * r;
             if (pair == 0 && g < rows) {
-                if (!whole) a.parts_lm[part_row + g] = make_float2(l[r], m[r]);
+                if (SHORT) lm_sh[warp][g] = make_float2(l[r], m[r]);
+                else if (!whole) a.parts_lm[part_row + g] = make_float2(l[r], m[r]);
                 else if (a.lse) a.lse[row0 + g] = log_sum(m[r], l[r]);
             }
+        }
+        if (SHORT) {
+            if (lane == 0) there[warp] = 1 + (int)(reinterpret_cast<char*>(out_sh) - mem);
+            break;
         }
         __syncwarp();
         const int c4 = s.dv / 4, pieces = rows * c4;
@@ -992,12 +1087,9 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
 #pragma unroll 1
         for (int i0 = 0; i0 < pieces; i0 += 32) {
             const int i = min(i0 + lane, pieces - 1), g = i / c4, c = i - g * c4;
-            auto piece = [&](int row) {
-                return *reinterpret_cast<const float4*>(out_sh + row * DP + ((c / 2 ^ (row & 7)) * 4 + (c & 1) * 2) * 2);
-            };
-            float4 v = piece(g);
+            float4 v = sums_at<DP>(out_sh, g, c);
             if (SETS == 1) {   // the copies of the rows carried the third term
-                const float4 u = piece(g + 4);
+                const float4 u = sums_at<DP>(out_sh, g + 4, c);
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
             }
             if (whole) {
@@ -1024,6 +1116,22 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
             __syncwarp();
         }
         now.skip(a, last - start, KEYS);
+    }
+    if (SHORT) {
+        __syncthreads();
+        const int g0 = unit.h * s.group + unit.rt * a.rows;
+        finish_unit<kBlockWarps, kRows>(
+            a, unit, (int64_t)unit.b * s.hq + g0, min(a.rows, s.group - unit.rt * a.rows), lm_sh, there, refs,
+            [&](int w, int g, int c) {
+                const float* sums = reinterpret_cast<const float*>(smem + w * MmaRing<DP>::kBytes + (there[w] - 1));
+                float4 v = sums_at<DP>(sums, g, c);
+                if (SETS == 1) {
+                    const float4 u = sums_at<DP>(sums, g + 4, c);
+                    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+                }
+                return v;
+            });
+        return;
     }
     if (a.csplits) grid_dependency_wait();
 }
@@ -1285,10 +1393,27 @@ wc_status resident_blocks(const void* kern, int threads, int smem, int* out) {
 
 using Kernel = void (*)(AttendArgs);
 
+// Steps of a warp up to which a table counts as short, where the units are
+// fewer than two an SM and where they are more.  Measured (with scores; one
+// launch against two): 8 heads of 256 tokens, bf16 7.7 us against 9.4, of 512
+// (8 steps) 11.8 against 9.6; 512 heads of 1024 tokens (16 steps) 49 against 60,
+// of 2048 84 against 69; fp32, half as many keys a step, alike by steps.
+constexpr int kShortSteps = 6, kShortStepsMany = 16;
+
 // Launches the coreset's kernel where there is one, the pages' (as many blocks
 // as the GPU holds at once, or one per tile where there are fewer), and the join.
-wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel core, int core_smem, cudaStream_t st) {
+wc_status run(AttendArgs a, Kernel pages, Kernel short_pages, int warps, int smem, int tile, Kernel core, int core_smem,
+              cudaStream_t st) {
     int room = 0, core_room = 0;
+    const int64_t all_units = (int64_t)a.s.B * a.s.hkv * a.row_tiles;
+    // Short tables without a coreset: a block for a unit, one launch and no partial rows.
+    const int steps = (a.s.cap + tile * warps - 1) / (tile * warps);
+    if (steps <= (all_units >= 2 * 148 ? kShortStepsMany : kShortSteps) && !a.csplits && !(a.scores && a.row_tiles > 1) && all_units <= INT32_MAX) {
+        if (resident_blocks(reinterpret_cast<const void*>(short_pages), warps * 32, smem, &room) != WC_OK ||
+            !launch(short_pages, all_units, warps * 32, smem, st, a))
+            return WC_ERR_CUDA;
+        return WC_OK;
+    }
     if (resident_blocks(reinterpret_cast<const void*>(pages), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
     const int64_t units = (int64_t)a.s.B * a.s.hkv * a.row_tiles, most = units * ((a.s.cap + tile - 1) / tile);
     const int64_t rows = (int64_t)a.s.B * a.s.hq, pairs = (int64_t)a.s.B * a.s.hkv;
@@ -1318,7 +1443,7 @@ wc_status run(AttendArgs a, Kernel pages, int warps, int smem, int tile, Kernel 
 
 template <int DP, int RG>
 wc_status run_simt(const AttendArgs& a, cudaStream_t st) {
-    return run(a, cache_attend_simt_kernel<DP, RG>, kSimtWarps, SimtSmem<DP, RG>::total, kSimtKeys,
+    return run(a, cache_attend_simt_kernel<DP, RG, false>, cache_attend_simt_kernel<DP, RG, true>, kSimtWarps, SimtSmem<DP, RG>::total, kSimtKeys,
                cache_coreset_kernel<float, RG, 8, DP>, CoresetSmem<float, 8, RG, DP>(a.s.d, a.s.dv).total, st);
 }
 
@@ -1335,7 +1460,7 @@ wc_status by_rows(const AttendArgs& a, cudaStream_t st) {
 template <int DP, int SETS>
 wc_status run_mma(const AttendArgs& a, cudaStream_t st) {
     constexpr int rows = SETS == 1 ? 4 : SETS == 2 ? 8 : 16;
-    return run(a, cache_attend_mma_kernel<DP, SETS>, kMmaWarps<DP>, kMmaWarps<DP> * MmaRing<DP>::kBytes, kMmaKeys,
+    return run(a, cache_attend_mma_kernel<DP, SETS, false>, cache_attend_mma_kernel<DP, SETS, true>, kMmaWarps<DP>, kMmaWarps<DP> * MmaRing<DP>::kBytes, kMmaKeys,
                cache_coreset_kernel<__nv_bfloat16, rows, 8, DP>,
                CoresetSmem<__nv_bfloat16, 8, rows, DP>(a.s.d, a.s.dv).total, st);
 }

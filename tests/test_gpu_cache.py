@@ -82,12 +82,30 @@ SHAPES = [
 ]
 
 
+# Tables of this many times the tokens: short ones take a block for each head,
+# long ones the division of all tiles and the join.
+ROOM = pytest.mark.parametrize("room", [1, 16])
+
+
+@ROOM
 @pytest.mark.parametrize("dtype,hq,hkv,d,dv,page,tf", SHAPES)
-def test_attend_shapes(dtype, hq, hkv, d, dv, page, tf):
+def test_attend_shapes(dtype, hq, hkv, d, dv, page, tf, room):
     """Head layouts, widths, page sizes and orders; lengths of 0, 1, about a
     tile's and a page's end, and several tiles."""
     lens = [0, 1, 15, 16, 17, 63, 64, 65, 130, 300]
-    case = Case(dtype, len(lens), hq, hkv, d, dv, page, -(-304 // page), lens, tokens_first=tf, seed=hq + d)
+    case = Case(dtype, len(lens), hq, hkv, d, dv, page, -(-304 * room // page), lens, tokens_first=tf, seed=hq + d)
+    check_attend(case)
+
+
+@pytest.mark.parametrize("dtype,dv,n", [(BF, 64, 384), (BF, 128, 385), (BF, 256, 576), (F32, 64, 192), (F32, 64, 193)])
+def test_attend_full_tables_about_the_short_ones_end(dtype, dv, n):
+    case = Case(dtype, 1, 4, 2, 64, dv, 1, n, [n], seed=n)
+    check_attend(case)
+
+
+def test_attend_many_short_heads():
+    """A table that is short for many heads only."""
+    case = Case(BF, 80, 4, 4, 16, 16, 32, 30, [(37 * i) % 961 for i in range(80)], seed=29)
     check_attend(case)
 
 
@@ -211,9 +229,10 @@ def test_attend_coreset_alone_equals_attend():
     assert float((out - want).abs().max() / want.abs().max()) <= 1e-5
 
 
-def test_attend_infinite_and_nan_inputs_stay_in_their_rows():
+@ROOM
+def test_attend_infinite_and_nan_inputs_stay_in_their_rows(room):
     """A NaN query row gives NaN there and nowhere else; -inf logits weigh 0."""
-    case = Case(F32, 2, 4, 2, 64, 64, 16, 20, [300, 200], seed=10)
+    case = Case(F32, 2, 4, 2, 64, 64, 16, 20 * room, [300, 200], seed=10)
     case.q[0, 1, 3] = float("nan")
     page, slot = int(case.table[1, 2]), 5
     case.k[page, 0, slot] = -float("inf")
@@ -230,8 +249,9 @@ def test_attend_infinite_and_nan_inputs_stay_in_their_rows():
     assert float((out.double() - want)[ok].abs().max()) <= 1e-5
 
 
-def test_attend_rows_that_are_all_minus_infinity():
-    case = Case(F32, 1, 1, 1, 8, 8, 16, 2, [20], seed=11)
+@ROOM
+def test_attend_rows_that_are_all_minus_infinity(room):
+    case = Case(F32, 1, 1, 1, 8, 8, 16, 20 * room, [20], seed=11)
     case.q[:] = 1.0
     case.k[~torch.isnan(case.k)] = -float("inf")
     cache, q, lens = make(case)
@@ -240,18 +260,20 @@ def test_attend_rows_that_are_all_minus_infinity():
     assert torch.equal(cache.scores.cpu(), case.scores)
 
 
+@ROOM
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_attend_strided_queries(dtype):
+def test_attend_strided_queries(dtype, room):
     """Queries as a slice of a projection's output, at an odd offset."""
-    case = Case(dtype, 3, 8, 2, 64, 64, 16, 20, [320, 7, 0], seed=12)
+    case = Case(dtype, 3, 8, 2, 64, 64, 16, 20 * room, [320, 7, 0], seed=12)
     cache, q, lens = make(case)
     wide = torch.zeros(3, 8, 64 + 11, dtype=dtype, device="cuda")
     wide[..., 3:67] = q
     assert torch.equal(cache.attend(wide[..., 3:67], lens), cache.attend(q, lens))
 
 
-def test_attend_bad_pages_and_lengths_are_reported_and_left_out():
-    case = Case(BF, 3, 8, 2, 64, 64, 16, 20, [320, 100, 50], seed=13)
+@ROOM
+def test_attend_bad_pages_and_lengths_are_reported_and_left_out(room):
+    case = Case(BF, 3, 8, 2, 64, 64, 16, 20 * room, [320, 100, 50], seed=13)
     cache, q, lens = make(case)
     good = cache.attend(q, lens)
     table = case.table.clone()
@@ -261,7 +283,7 @@ def test_attend_bad_pages_and_lengths_are_reported_and_left_out():
     assert cache.check() == 7 and cache.check() == 0
     assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
     # sequence 1 without tokens 32..47
-    ref = Case(BF, 3, 8, 2, 64, 64, 16, 20, [320, 100, 50], seed=13)
+    ref = Case(BF, 3, 8, 2, 64, 64, 16, 20 * room, [320, 100, 50], seed=13)
     k, v = [], []
     for h in range(2):
         kk, vv = ref.rows(1, h)
@@ -591,10 +613,11 @@ def test_evict_refuses_shared_and_bad_pages():
     assert cache.check() == 7 and res["lens"].tolist() == [16, 160, 16]
 
 
-def test_shared_pages_are_read_alike():
+@ROOM
+def test_shared_pages_are_read_alike(room):
     """Two sequences with the same pages attend to the same rows, and each
     accumulates its own scores."""
-    case = Case(BF, 2, 4, 2, 64, 64, 16, 10, [150, 150], seed=19)
+    case = Case(BF, 2, 4, 2, 64, 64, 16, 10 * room, [150, 150], seed=19)
     case.table[1] = case.table[0]
     case.q[1] = case.q[0]
     cache, q, lens = make(case)
@@ -603,11 +626,12 @@ def test_shared_pages_are_read_alike():
     assert torch.equal(out[0], out[1]) and torch.equal(cache.scores[0], cache.scores[1])
 
 
-def test_captured_step_serves_a_growing_cache():
+@ROOM
+def test_captured_step_serves_a_growing_cache(room):
     """append, attend and the length's advance captured once, replayed over
     eight tokens: the same bits as eager calls on a copy of the cache."""
     def cache_of():
-        case = Case(BF, 2, 8, 2, 64, 64, 16, 8, [128, 128], seed=20)
+        case = Case(BF, 2, 8, 2, 64, 64, 16, 8 * room, [128, 128], seed=20)
         cache, _, _ = make(case)
         return cache, torch.tensor([30, 61], dtype=torch.int32, device="cuda")
 
@@ -694,13 +718,14 @@ def test_other_stream():
     assert torch.equal(out, want) and res["lens"].tolist() == [100, 100, 0, 5]
 
 
+@ROOM
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_serving_run(dtype):
+def test_serving_run(dtype, room):
     """Prompt, decode steps with accumulation, eviction, more steps: against
     the same run in 64 bits (its own scores decide its evictions; the scores
     are far enough apart for both to keep the same tokens)."""
     B, hq, hkv, d, page, keep = 2, 4, 2, 64, 16, 40
-    case = Case(dtype, B, hq, hkv, d, d, page, 8, [128] * B, seed=22)
+    case = Case(dtype, B, hq, hkv, d, d, page, 8 * room, [128] * B, seed=22)
     case.scores.zero_()
     cache, _, _ = make(case)
     g = torch.Generator().manual_seed(2)
