@@ -90,10 +90,10 @@ __device__ __forceinline__ void tile_logits(const char* krows, int k_row, const 
 // A warp's way through its tiles: the stretch, the unit (sequence b, kv head h,
 // row tile rt) and the tile k of its `tiles`.
 struct Walk {
-    int left;          // tiles to the end of the stretch, this one included
+    int left;          // places to the end of the stretch, from this tile's on
     int stretch;
     int b, h, rt, k, tiles, len;
-    // to the first tile of stretch c; pre: the tiles before every step-th sequence
+    // to the first tile of stretch c; pre: the places before every step-th sequence
     __device__ __forceinline__ void start(const AttendArgs& a, const Share& share, const int* pre, int step, int c,
                                           int tile) {
         stretch = c;
@@ -103,22 +103,27 @@ struct Walk {
         int t = share.first(c);
         left = share.last(c) - t;
         const int per_tile = a.s.hkv * a.row_tiles;
-        int lo = 0, hi = (a.s.B + step - 1) / step;   // the last place with no more than t tiles before it
+        int lo = 0, hi = (a.s.B + step - 1) / step;   // the last of them with no more than t places before it
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (pre[mid] <= t) lo = mid;
             else hi = mid;
         }
         t -= pre[lo];
+        int places = 0;
         for (b = lo * step;; ++b) {
             len = checked_len(a.lens, b, a.s.cap, a.status);
-            const int n = (len + tile - 1) / tile * per_tile;
-            if (t < n) break;
-            t -= n;
+            places = (int)unit_places(len, tile);
+            if (t < places * per_tile) break;
+            t -= places * per_tile;
         }
-        tiles = (len + tile - 1) / tile;
-        const int unit = t / tiles;
-        k = t - unit * tiles;
+        tiles = places - kUnitCost;
+        const int unit = t / places;
+        k = t - unit * places - kUnitCost;
+        if (k < 0) {   // in the places before its tiles
+            left += k;
+            k = 0;
+        }
         h = unit / a.row_tiles;
         rt = unit - h * a.row_tiles;
     }
@@ -139,6 +144,8 @@ struct Walk {
         left -= n;
         k += n;
         if (left <= 0 || k < tiles) return false;
+        left -= kUnitCost;
+        if (left <= 0) return false;
         k = 0;
         if (++rt == a.row_tiles) {
             rt = 0;
@@ -1189,7 +1196,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) cache_join_kernel(const Atten
         const int in_b = h * a.row_tiles + rt;
         n_pages = 0;
         if (tiles > 0) {
-            const int t0 = at.before + in_b * tiles, c0 = share.of(t0), c1 = share.of(t0 + tiles - 1);
+            const int t0 = at.before + in_b * (tiles + kUnitCost) + kUnitCost;
+            const int c0 = share.of(t0), c1 = share.of(t0 + tiles - 1);
             if (c0 == c1 && !a.csplits && !a.logits) return false;   // finished by the warp itself
             page0 = ((int64_t)b * per_tile + in_b + c0) * a.rows + in_unit;
             n_pages = c1 - c0 + 1;
@@ -1395,10 +1403,11 @@ using Kernel = void (*)(AttendArgs);
 
 // Steps of a warp up to which a table counts as short, where the units are
 // fewer than two an SM and where they are more.  Measured (with scores; one
-// launch against two): 8 heads of 256 tokens, bf16 7.7 us against 9.4, of 512
-// (8 steps) 11.8 against 9.6; 512 heads of 1024 tokens (16 steps) 49 against 60,
-// of 2048 84 against 69; fp32, half as many keys a step, alike by steps.
-constexpr int kShortSteps = 6, kShortStepsMany = 16;
+// launch against two): 8 heads of 256 tokens, bf16 7.7 us against 9.3, of 512
+// (8 steps) 12.0 against 9.6; 512 heads of up to 256 tokens 17.7 us against 22.3,
+// of 512 27.5 against 28.0, of 1024 (16 steps) 49 against 42; fp32, half as many
+// keys a step, alike by steps.
+constexpr int kShortSteps = 6, kShortStepsMany = 8;
 
 // Launches the coreset's kernel where there is one, the pages' (as many blocks
 // as the GPU holds at once, or one per tile where there are fewer), and the join.
@@ -1415,7 +1424,7 @@ wc_status run(AttendArgs a, Kernel pages, Kernel short_pages, int warps, int sme
         return WC_OK;
     }
     if (resident_blocks(reinterpret_cast<const void*>(pages), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
-    const int64_t units = (int64_t)a.s.B * a.s.hkv * a.row_tiles, most = units * ((a.s.cap + tile - 1) / tile);
+    const int64_t units = all_units, most = units * unit_places(a.s.cap, tile);
     const int64_t rows = (int64_t)a.s.B * a.s.hq, pairs = (int64_t)a.s.B * a.s.hkv;
     // score blocks of one (sequence, kv head): a stretch each, at most about 4096 blocks in all
     const int64_t chunks = min((int64_t)(a.s.cap + kScoreKeys - 1) / kScoreKeys, (4096 + pairs - 1) / pairs);

@@ -143,31 +143,38 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Division of the batch's work.  The keys of every unit (sequence, kv head,
-// row tile of its group's queries) are cut into tiles, all T tiles stand in one
-// row, ordered by unit, and each warp takes one stretch of `per` tiles, so that
-// all have equal work whatever the lengths are.  A unit that spans several
-// stretches leaves one set of partial rows for each; the set of unit u from
-// stretch c has slot u + c, which no other pair has: along the row each next set
-// has a larger u, a larger c or both.
+// row tile of its group's queries) are cut into tiles, all tiles stand in one
+// row, ordered by unit, with kUnitCost empty places before each unit's, and each
+// warp takes one stretch of `per` places, so that all have equal work whatever
+// the lengths are.  (The empty places stand for what a unit costs beside its
+// tiles, its queries and its partial rows: without them a warp that meets a
+// sequence of a few tokens has a unit at every tile and ends long after the
+// others, 52 us against 31 in a batch of 64 with such a one.)
+// A unit that spans several stretches leaves one set of partial rows for each;
+// the set of unit u from stretch c has slot u + c, which no other pair has: along
+// the row each next set has a larger u, a larger c or both.
 // (The SMs do not get equal shares of the memory's rate: the slowest warp ends
 // at 1.15 times the mean.  Measured and not kept: four fifths of the work divided
 // so and the rest in short stretches that warps take from a counter; going on to
 // another stretch stalls a warp for longer than the evenness saves, 94 -> 106 us
 // for four sequences of 32768 tokens.)
 constexpr int kPlaces = 1024;      // places in the row that a block holds: every sequence's, or every n-th one's
+constexpr int kUnitCost = 4;       // in tiles (of 1, 2, 4, 8 measured)
+// Places of one unit of n tokens.
+__host__ __device__ __forceinline__ int64_t unit_places(int n, int tile) { return n > 0 ? ((int64_t)n + tile - 1) / tile + kUnitCost : 0; }
 struct Share {
-    int total, per, count;   // tiles, tiles of a stretch, stretches
-    __device__ __forceinline__ Share(int tiles, int warps)
-        : total(tiles), per(max((tiles + warps - 1) / warps, 1)), count((tiles + per - 1) / per) {}
+    int total, per, count;   // places, places of a stretch, stretches
+    __device__ __forceinline__ Share(int places, int warps)
+        : total(places), per(max((places + warps - 1) / warps, 1)), count((places + per - 1) / per) {}
     __device__ __forceinline__ int first(int c) const { return c * per; }
     __device__ __forceinline__ int last(int c) const { return min(c * per + per, total); }
     __device__ __forceinline__ int of(int t) const { return t / per; }
 };
 
-// Tiles of the batch and the tiles before sequence want_b (where >= 0); where
-// pre is not null, the tiles before every step-th sequence go there.  All threads of the
+// Places of the batch and those before sequence want_b (where >= 0); where pre
+// is not null, those before every step-th sequence go there.  All threads of the
 // block call it; `sh` holds an int and one per warp.  The host has seen to it
-// that the tiles of full tables stay below 2^31.
+// that the places of full tables stay below 2^31.
 struct Place { int total, before; };
 
 template <int THREADS>
@@ -176,7 +183,7 @@ __device__ Place scan_tiles(const View& s, const int32_t* lens, int tile, int pe
     const int per = (s.B + THREADS - 1) / THREADS;
     const int b0 = threadIdx.x * per, b1 = min(b0 + per, s.B);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += (checked_len(lens, b, s.cap, status) + tile - 1) / tile * per_tile;
+    for (int b = b0; b < b1; ++b) sum += (int)unit_places(checked_len(lens, b, s.cap, status), tile) * per_tile;
     int incl = sum;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -196,7 +203,7 @@ __device__ Place scan_tiles(const View& s, const int32_t* lens, int tile, int pe
         for (int b = b0; b < b1; ++b) {
             if (pre && b % step == 0) pre[b / step] = at;
             if (b == want_b) sh[0] = at;
-            at += (checked_len(lens, b, s.cap, status) + tile - 1) / tile * per_tile;
+            at += (int)unit_places(checked_len(lens, b, s.cap, status), tile) * per_tile;
         }
     __syncthreads();
     return Place{total, want_b >= 0 ? sh[0] : 0};

@@ -105,7 +105,7 @@ def test_attend_full_tables_about_the_short_ones_end(dtype, dv, n):
 
 def test_attend_many_short_heads():
     """A table that is short for many heads only."""
-    case = Case(BF, 80, 4, 4, 16, 16, 32, 30, [(37 * i) % 961 for i in range(80)], seed=29)
+    case = Case(BF, 80, 4, 4, 16, 16, 32, 16, [(37 * i) % 513 for i in range(80)], seed=29)
     check_attend(case)
 
 
