@@ -1,6 +1,6 @@
 // wc_cache.cuh — what the paged-cache kernels share: the kernels' view of the
 // cache, checked lengths and page lookups, the even division of the batch's
-// key tiles over the thread blocks, and asynchronous row loads.
+// key tiles over the warps, asynchronous copies and dependent launches.
 #pragma once
 
 #include <math_constants.h>

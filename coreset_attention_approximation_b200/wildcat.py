@@ -427,6 +427,7 @@ class PagedCache:
         self._room = (self.ws.data_ptr(), n)
         self._q_shape, self._o_shape = (self.batch, self.hq, self.d), (self.batch, self.hq, self.dv)
         self._seqs, self._index = (self.batch,), self.device.index
+        self._k_row, self._v_row = WcRowStrides(hkv * d, d, d), WcRowStrides(hkv * self.dv, self.dv, self.dv)
         self._kept = (self.k_pages, self.v_pages, self.table, self.scores, self.ws)
         L = lib()
         self._append, self._attend, self._evict = L.wc_cache_append, L.wc_cache_attend, L.wc_cache_evict
@@ -499,7 +500,10 @@ class PagedCache:
         self._tensor(pos, "pos", self._seqs, torch.int32)
         if count is not None:
             self._tensor(count, "count", self._seqs, torch.int32)
-        ks, vs = WcRowStrides(*_strides(K)), WcRowStrides(*_strides(V))
+        if t == 1 and K.is_contiguous() and V.is_contiguous():     # a decode step's rows
+            ks, vs = self._k_row, self._v_row
+        else:
+            ks, vs = WcRowStrides(*_strides(K)), WcRowStrides(*_strides(V))
         self._launch(self._append, "wc_cache_append", stream,
                      (self._shape_ref, t, K.data_ptr(), ks, V.data_ptr(), vs, pos.data_ptr(),
                       None if count is None else count.data_ptr(), *self._pools, self._p_scores, *self._room),
