@@ -478,6 +478,16 @@ __device__ bool refused(const EvictArgs& a, int b, int len, int kept) {
     return true;
 }
 
+// One int32, whole, where another block may write or read it at the same time.
+__device__ __forceinline__ int load_relaxed(const int32_t* p) {
+    int x;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+__device__ __forceinline__ void store_relaxed(int32_t* p, int x) {
+    asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
+}
+
 // The scores of one (sequence, kv head), a stretch read whole before it is
 // written (see move_in_place), its lengths, and -1 in idx where refused.
 __device__ void move_scores(const EvictArgs& a, int b, int h, int len, int kept, bool no, char* stage) {
@@ -485,8 +495,8 @@ __device__ void move_scores(const EvictArgs& a, int b, int h, int len, int kept,
     const int64_t unit = (int64_t)b * s.hkv + h;
     int32_t* idx = a.idx + unit * a.keep;
     if (h == 0 && threadIdx.x == 0) a.lens_out[b] = no ? len : kept;
-    if (no) {   // (the blocks that move rows are refused too and do not read idx)
-        for (int j = threadIdx.x; j < a.keep; j += kMoveThreads) idx[j] = -1;
+    if (no) {   // (blocks that move rows may read idx at the same time: see cache_move_kernel)
+        for (int j = threadIdx.x; j < a.keep; j += kMoveThreads) store_relaxed(idx + j, -1);
         return;
     }
     if (len <= kept && a.scores_into == a.scores) return;
@@ -555,11 +565,16 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const EvictArg
     if (part == 0 && h == 0 && b == 0 && threadIdx.x == 0) a.phase[0] = a.phase[1] ^ 1;
     constexpr int kBlockRows = kMoveThreads / 32 * kCopyRows;
     if (part > 0 && (a.into ? (part - 1) * kBlockRows >= kept : len <= kept)) return;
-    // where a lane's row comes from and goes to, on its way while the pages are checked
+    // Where a lane's row comes from and goes to, on its way while the pages are checked.  The sequence may
+    // be refused, and then the block that takes the scores writes -1 over idx, before or after this block reads
+    // it: only a position of the sequence is looked up (and nothing of it is used once this block has found the
+    // refusal itself).  In place, rows are read from idx behind the check alone.
     const int lane = threadIdx.x & 31, j = (part - 1) * kBlockRows + (threadIdx.x >> 5) * kCopyRows + lane;
     RowCopy r{nullptr, nullptr, nullptr, nullptr, false};
-    if (part > 0 && a.into && lane < kCopyRows && j < kept) {
-        const int at = a.idx[((int64_t)b * s.hkv + h) * a.keep + j], tp = page_of(s, at), slot = at - tp * s.page;
+    int at = -1;
+    if (part > 0 && a.into && lane < kCopyRows && j < kept) at = load_relaxed(a.idx + ((int64_t)b * s.hkv + h) * a.keep + j);
+    if ((unsigned)at < (unsigned)len) {
+        const int tp = page_of(s, at), slot = at - tp * s.page;
         const int to = page_of(s, j), to_slot = j - to * s.page;
         const int64_t from_page = s.table[(int64_t)b * s.max_pages + tp], to_page = a.into[(int64_t)b * s.max_pages + to];
         r.ks = a.kp + from_page * s.k_page + h * s.k_head + (int64_t)slot * s.k_token;

@@ -1,0 +1,56 @@
+"""The paged cache on the GPU at its edges: what the calls promise for refused
+sequences, extreme values, other streams and rows outside the cache."""
+
+import numpy as np
+import pytest
+import torch
+
+import cache_ref
+from coreset_attention_approximation_b200 import wildcat
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def test_evict_into_refuses_a_few_of_many():
+    """More blocks than the GPU holds at once, thousands of kept rows, and a
+    few sequences refused for each reason: those stay as they are, and every
+    other one is moved."""
+    B, hkv, page, d, n, keep = 64, 8, 16, 8, 3000, 2500
+    g = torch.Generator().manual_seed(1)
+    m = -(-n // page)
+    order = torch.randperm(2 * B * m, generator=g).to(torch.int32)
+    table, into = order[: B * m].reshape(B, m).clone(), order[B * m:].reshape(B, m).clone()
+    k0 = torch.randn(2 * B * m, hkv, page, d, generator=g).to(BF)
+    v0 = torch.randn(2 * B * m, hkv, page, d, generator=g).to(BF)
+    s0 = torch.rand(B, hkv, m * page, generator=g)
+    used = -(-keep // page)
+    into[3, used - 1] = 2 * B * m                # no page
+    into[17, 5] = into[18, 6]                    # one page for two sequences
+    into[40, 0] = into[40, 1]                    # and for two places of one
+    into[41, 2] = table[7, 9]                    # a page that is read
+    table[63, m - 1] = -9                        # no page among those read
+    refused = [3, 17, 18, 40, 41, 63]
+    lens = torch.full((B,), n, dtype=torch.int32)
+    k, v, scores = k0.cuda(), v0.cuda(), s0.cuda()
+    to = torch.full_like(scores, -7.0)
+    cache = wildcat.PagedCache(k, v, table.cuda(), hq=hkv, scores=scores)
+    res = cache.evict(lens.cuda(), keep, sink=4, recent=64, into=into.cuda(), scores_into=to)
+    assert cache.check() in (1, 7)               # (the first that was recorded)
+    idx, new = res["idx"].cpu(), res["lens"].tolist()
+    want_k, want_v, want_s = k0.clone(), v0.clone(), torch.full_like(s0, -7.0)
+    at = torch.arange(keep)
+    for b in range(B):
+        assert new[b] == (n if b in refused else keep)
+        if b in refused:
+            assert torch.all(idx[b] == -1)
+            continue
+        for h in range(hkv):
+            src = torch.from_numpy(cache_ref.kept_positions(s0[b, h].numpy(), n, keep, 4, 64))
+            assert torch.equal(idx[b, h].long(), src)
+            f, t = table[b].long()[src // page], into[b].long()[at // page]
+            want_k[t, h, at % page], want_v[t, h, at % page] = k0[f, h, src % page], v0[f, h, src % page]
+            want_s[b, h, :keep] = s0[b, h, src]
+    assert torch.equal(k.cpu(), want_k) and torch.equal(v.cpu(), want_v) and torch.equal(to.cpu(), want_s)
+    assert torch.equal(scores.cpu(), s0)
