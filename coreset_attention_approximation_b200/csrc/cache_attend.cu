@@ -350,21 +350,23 @@ __device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, u
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
 
-// The three bf16 terms of a pair of weights, x = t0 + t1 + t2 up to 2^-24 x:
-// one term alone (half a step, 2^-9 relative) would be the largest error of the
-// whole attention, whose output is fp32.
+// The three bf16 terms of a pair of weights x >= 0, x = t0 + t1 + t2: the upper 8
+// bits of x, of the rest and of the rest of that (one rounded term alone, half a
+// step or 2^-9 relative, would be the largest error of the whole attention, whose
+// output is fp32).  Cut off, not rounded, so that no term is negative, and none is
+// below kLeast = 2^-126: an infinite value then meets only positive factors and
+// its column is infinite, as by the definition (0 inf and inf - inf are NaN).  A
+// weight that is 0 because it is below 2^-126 grows by that much at most; rows that
+// are not there are zeros.  NaN stays NaN.
+constexpr uint32_t kLeast = 0x00800080u;   // a pair of bf16 2^-126
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t t[3]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        t[i] = pack_bf16(x, y);
-        x -= __uint_as_float(t[i] << 16);
-        y -= __uint_as_float(t[i] & 0xffff0000u);
+        const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(t[i]) : "r"(__byte_perm(a, b, 0x7632)), "r"(kLeast));
+        x -= __uint_as_float(a & 0xffff0000u);
+        y -= __uint_as_float(b & 0xffff0000u);
     }
 }
 
@@ -1026,10 +1028,10 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
             const int row = lane & 15;
             const uint32_t base = vd + row * kRow;
             uint32_t p0 = 0, p1 = 0, p2 = 0, p3 = 0;
-            if (SETS == 1) {   // rows 0-3: term 0, 8-11: term 1, 4-7: term 2, 12-15: nothing
+            if (SETS == 1) {   // rows 0-3: term 0, 8-11: term 1, 4-7: term 2, 12-15: as good as nothing
                 const bool up = quad < 4;
-                p0 = up ? w[0][0][0] : w[0][0][2]; p1 = up ? w[0][0][1] : 0u;
-                p2 = up ? w[0][1][0] : w[0][1][2]; p3 = up ? w[0][1][1] : 0u;
+                p0 = up ? w[0][0][0] : w[0][0][2]; p1 = up ? w[0][0][1] : kLeast;
+                p2 = up ? w[0][1][0] : w[0][1][2]; p3 = up ? w[0][1][1] : kLeast;
             }
 #pragma unroll
             for (int n = 0; n < DP / 16; ++n) {
@@ -1047,7 +1049,7 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
                         mma16816_new(z, p0, p1, p2, p3, b0, b1);
                     } else if (SETS == 2) {
                         mma16816_new(z, w[0][0][0], w[0][0][1], w[0][1][0], w[0][1][1], b0, b1);
-                        mma16816(z, w[0][0][2], 0u, w[0][1][2], 0u, b0, b1);
+                        mma16816(z, w[0][0][2], kLeast, w[0][1][2], kLeast, b0, b1);
                     } else {
                         mma16816_new(z, w[0][0][0], w[kMine - 1][0][0], w[0][1][0], w[kMine - 1][1][0], b0, b1);
                         mma16816(z, w[0][0][1], w[kMine - 1][0][1], w[0][1][1], w[kMine - 1][1][1], b0, b1);

@@ -333,7 +333,10 @@ wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const
  *   L = sum_i a_i + sum_s a'_s W[s, dv]
  *   out[b, g, :] = (sum_i a_i v_i + sum_s a'_s W[s, :dv]) / L,  lse[b, g] = log L
  * out [B, Hq, dv] fp32, lse [B, Hq] fp32 or NULL.  A sequence without tokens
- * (and without coreset rows) gets out = 0, lse = -inf.  With scores (not NULL)
+ * (and without coreset rows) gets out = 0, lse = -inf.  An infinite value makes
+ * its column infinite for the kv head's queries (infinities of both signs, or a
+ * NaN: NaN) and touches nothing else; where its weight beside the row's largest
+ * underflows fp32, the column is infinite or NaN.  With scores (not NULL)
  *   scores[b, h, i] += sum over the queries g of kv head h of a_i / L,
  * positions from lens[b] on left as they were.  The sums are split over the
  * blocks of the launch and joined in a fixed order: results repeat bit for bit

@@ -54,3 +54,43 @@ def test_evict_into_refuses_a_few_of_many():
             want_s[b, h, :keep] = s0[b, h, src]
     assert torch.equal(k.cpu(), want_k) and torch.equal(v.cpu(), want_v) and torch.equal(to.cpu(), want_s)
     assert torch.equal(scores.cpu(), s0)
+
+
+ROOM = pytest.mark.parametrize("room", [1, 16])   # short tables (one launch) and long ones (divided and joined)
+
+
+@ROOM
+@pytest.mark.parametrize("dtype,group", [(BF, 1), (BF, 4), (BF, 7), (BF, 8), (BF, 16), (BF, 20), (F32, 3), (F32, 16)])
+@pytest.mark.parametrize("equal", [False, True])
+def test_attend_infinite_values(dtype, group, equal, room):
+    """An infinite value makes its column infinite for the queries of its kv
+    head (both infinities, or a NaN: NaN), and changes no bit of anything else.
+    With equal keys every weight is exact in 8 bits."""
+    case = cache_ref.Case(dtype, 3, 2 * group, 2, 64, 48, 16, 20 * room, [300, 77, 16], seed=group)
+    if equal:
+        case.k[~torch.isnan(case.k)] = 0.25
+
+    def run():
+        k, v, table, q, lens, _ = case.on_gpu()
+        cache = wildcat.PagedCache(k, v, table, hq=2 * group)
+        out = cache.attend(q, lens)
+        assert cache.check() == 0
+        return out.cpu()
+
+    clean = run()
+    assert torch.isfinite(clean).all()
+    inf, at = float("inf"), lambda b, t: (int(case.table[b, t // 16]), 1, t % 16)      # kv head 1
+    case.v[at(0, 3)][0] = inf
+    case.v[at(0, 299)][47] = inf
+    case.v[at(0, 200)][9] = -inf
+    case.v[at(0, 17)][30], case.v[at(0, 170)][30] = inf, -inf
+    case.v[at(0, 40)][31] = float("nan")
+    case.v[at(2, 15)][5], case.v[at(2, 0)][5] = -inf, -inf
+    got = run()
+    want = clean.clone()
+    heads = slice(group, 2 * group)
+    want[0, heads, 0], want[0, heads, 47], want[0, heads, 9], want[2, heads, 5] = inf, inf, -inf, -inf
+    want[0, heads, 30] = want[0, heads, 31] = float("nan")
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got, nan=0.5, posinf=inf, neginf=-inf),
+                       torch.nan_to_num(want, nan=0.5, posinf=inf, neginf=-inf))
