@@ -28,6 +28,13 @@ namespace {
 
 constexpr int kSimtWarps = 4;
 
+// A running row's reference is set this far (in log2 units) above the largest
+// logit, and moves only when a logit passes it: most steps are spared the
+// rescaling.  Above and not below it, so that no weight exceeds 1 and a value's
+// product with it overflows only where the value does (weights of up to 2^8
+// overflowed from |v| = 2^120 on); a weight underflows below 2^-118 of the largest.
+constexpr float kAhead = 8.f;
+
 // Pairs of fp32 values in one 64-bit register, added and multiplied as one:
 // half the instructions where the issue of sums is what bounds a loop.
 __device__ __forceinline__ uint64_t pair_of(float x, float y) {
@@ -539,10 +546,10 @@ __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const
                 float top = fmaxf(y[0], y[1]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const bool grow = top > m[r] + 8.f;   // (the reference follows when the maximum has grown by 2^8)
+                const bool grow = top > m[r];
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? ex2(m[r] - top) : 1.f;
-                    if (grow) m[r] = top;
+                    const float f = grow ? ex2(m[r] - (top + kAhead)) : 1.f;
+                    if (grow) m[r] = top + kAhead;
 #pragma unroll
                     for (int g = 0; g < (RG < 8 ? RG : 8); ++g) rescale((g + 8 * r) % RG, __shfl_sync(0xffffffffu, f, g * 4));
                 }
@@ -786,9 +793,9 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_attend_simt_kernel(cons
             float top = x[g];
 #pragma unroll
             for (int e = 1; e < KEYS; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-            if (top > m[g] + 8.f) {   // (the reference follows the maximum when it has grown by 2^8, see below)
-                const float f = ex2(m[g] - top);   // 0 where nothing was summed yet
-                m[g] = top;
+            if (top > m[g]) {
+                const float f = ex2(m[g] - (top + kAhead));   // 0 where nothing was summed yet
+                m[g] = top + kAhead;
                 l[g] *= f;
 #pragma unroll
                 for (int i = 0; i < kCols * 2; ++i) o[g][i] = mul2(o[g][i], pair_of(f, f));
@@ -1002,12 +1009,10 @@ __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(co
             float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // The reference follows the maximum only when it has grown by more than 2^8, which
-            // spares most steps the rescaling; weights up to 2^8 lose nothing in fp32.
-            const bool grow = top > m[r] + 8.f;
+            const bool grow = top > m[r];
             if (__any_sync(0xffffffffu, grow)) {
-                const float f = grow ? ex2(m[r] - top) : 1.f;
-                if (grow) m[r] = top;
+                const float f = grow ? ex2(m[r] - (top + kAhead)) : 1.f;
+                if (grow) m[r] = top + kAhead;
                 l[r] *= f;
                 const uint64_t ff = pair_of(f, f);
 #pragma unroll

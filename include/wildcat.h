@@ -335,8 +335,9 @@ wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const
  * out [B, Hq, dv] fp32, lse [B, Hq] fp32 or NULL.  A sequence without tokens
  * (and without coreset rows) gets out = 0, lse = -inf.  An infinite value makes
  * its column infinite for the kv head's queries (infinities of both signs, or a
- * NaN: NaN) and touches nothing else; where its weight beside the row's largest
- * underflows fp32, the column is infinite or NaN.  With scores (not NULL)
+ * NaN: NaN) and touches nothing else; where its weight is below 2^-118 of the
+ * row's largest, the column is infinite or NaN, and a finite value may count as
+ * 0 there.  The weights in the fp32 sums are at most 1.  With scores (not NULL)
  *   scores[b, h, i] += sum over the queries g of kv head h of a_i / L,
  * positions from lens[b] on left as they were.  The sums are split over the
  * blocks of the launch and joined in a fixed order: results repeat bit for bit

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import cache_bounds
 import cache_ref
 from coreset_attention_approximation_b200 import wildcat
 
@@ -94,3 +95,36 @@ def test_attend_infinite_values(dtype, group, equal, room):
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(torch.nan_to_num(got, nan=0.5, posinf=inf, neginf=-inf),
                        torch.nan_to_num(want, nan=0.5, posinf=inf, neginf=-inf))
+
+
+@ROOM
+@pytest.mark.parametrize("dtype,group", [(BF, 2), (BF, 8), (BF, 16), (F32, 1), (F32, 4), (F32, 8)])
+@pytest.mark.parametrize("r", [0, 200])
+def test_attend_huge_values(dtype, group, r, room):
+    """Values about 2^121 and logits that rise by 5 behind the first tiles of a
+    warp: no product may overflow, in the pages or in a coreset.  600 sequences
+    with the same pages, so that every warp has several tiles."""
+    B, n, d = 600, 300, 64
+    case = cache_ref.Case(dtype, 1, group, 1, d, d, 16, 20 * room, [n], seed=3)
+    case.k = 0.125 * torch.round(case.k.float())                   # (unused slots stay NaN)
+    for t in range(n):
+        case.k[int(case.table[0, t // 16]), 0, t % 16, 0] = 0.0 if t < 64 else 5.0
+    case.k = case.k.to(dtype)
+    case.q[..., 0] = 8.0                                           # beta <q, k> = k[0] + noise
+    case.v = (case.v.float() * 2.0 ** 120).to(dtype)
+    core = None
+    if r:
+        g = torch.Generator().manual_seed(5)
+        Ks = 0.125 * torch.round(torch.randn(1, 1, r, d, generator=g))
+        Ks[..., 0] = 5.0 * (torch.arange(r) // 32 % 2)
+        w = 1.0 + torch.rand(1, 1, r, 1, generator=g)
+        core = (Ks.to(dtype), torch.cat([w * torch.randn(1, 1, r, d, generator=g) * 2.0 ** 120, w], -1), None)
+    many = lambda x: x.cuda().expand(B, *x.shape[1:]).contiguous()
+    cache = wildcat.PagedCache(case.k.cuda(), case.v.cuda(), many(case.table), hq=group, scores=many(case.scores))
+    out, lse = cache.attend(many(case.q), many(case.lens), coreset=core and (many(core[0]), many(core[1]), None),
+                            accumulate=True, return_lse=True)
+    assert cache.check() == 0
+    ref = cache_bounds.attend(case, core)
+    cache_bounds.check(out, ref["out"], ref["out_b"], "out")
+    cache_bounds.check(lse, ref["lse"], ref["lse_b"], "lse")
+    cache_bounds.check(cache.scores.cpu().double() - case.scores.double(), ref["wts"], ref["wts_b"], "scores")
