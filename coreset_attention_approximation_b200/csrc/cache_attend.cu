@@ -1430,7 +1430,6 @@ wc_status run(AttendArgs a, Kernel pages, Kernel short_pages, int warps, int sme
             return WC_ERR_CUDA;
         return WC_OK;
     }
-    if (resident_blocks(reinterpret_cast<const void*>(pages), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
     const int64_t units = all_units, most = units * unit_places(a.s.cap, tile);
     const int64_t rows = (int64_t)a.s.B * a.s.hq, pairs = (int64_t)a.s.B * a.s.hkv;
     // score blocks of one (sequence, kv head): a stretch each, at most about 4096 blocks in all
@@ -1443,9 +1442,10 @@ wc_status run(AttendArgs a, Kernel pages, Kernel short_pages, int warps, int sme
     while (cols && cols < a.s.dv && rows * ((a.s.dv + cols - 1) / cols) > most_blocks) cols *= 2;
     const int64_t join = (cols ? rows * ((a.s.dv + cols - 1) / cols) : (int64_t)a.s.B * ((a.s.hq + kJoinWarps - 1) / kJoinWarps)) +
                          (a.scores ? chunks * pairs : 0);
-    if (most > INT32_MAX || join > INT32_MAX) return WC_ERR_UNSUPPORTED;   // (tiles are counted in 32 bits)
+    // (places are counted in 32 bits, also where they are rounded up to a multiple of the warps)
+    if (most + max_warps(a.s) > INT32_MAX || join > INT32_MAX || units * a.csplits > INT32_MAX) return WC_ERR_UNSUPPORTED;
+    if (resident_blocks(reinterpret_cast<const void*>(pages), warps * 32, smem, &room) != WC_OK) return WC_ERR_CUDA;
     if (a.csplits) {
-        if (units * a.csplits > INT32_MAX) return WC_ERR_UNSUPPORTED;
         if (resident_blocks(reinterpret_cast<const void*>(core), kCoresetWarps * 32, core_smem, &core_room) != WC_OK ||
             !launch(core, units * a.csplits, kCoresetWarps * 32, core_smem, st, a))
             return WC_ERR_CUDA;

@@ -167,14 +167,14 @@ struct Share {
     __device__ __forceinline__ Share(int places, int warps)
         : total(places), per(max((places + warps - 1) / warps, 1)), count((places + per - 1) / per) {}
     __device__ __forceinline__ int first(int c) const { return c * per; }
-    __device__ __forceinline__ int last(int c) const { return min(c * per + per, total); }
+    __device__ __forceinline__ int last(int c) const { return first(c) + min(per, total - first(c)); }
     __device__ __forceinline__ int of(int t) const { return t / per; }
 };
 
 // Places of the batch and those before sequence want_b (where >= 0); where pre
 // is not null, those before every step-th sequence go there.  All threads of the
 // block call it; `sh` holds an int and one per warp.  The host has seen to it
-// that the places of full tables stay below 2^31.
+// that the places of full tables and the warps together stay below 2^31.
 struct Place { int total, before; };
 
 template <int THREADS>

@@ -341,7 +341,9 @@ wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const
  *   scores[b, h, i] += sum over the queries g of kv head h of a_i / L,
  * positions from lens[b] on left as they were.  The sums are split over the
  * blocks of the launch and joined in a fixed order: results repeat bit for bit
- * for the same lengths, shape and GPU.
+ * for the same lengths, shape and GPU.  Tables with room for B * Hkv * cap of
+ * about 2^34 tokens and more (fp32: 2^33; proportionally fewer where more than 16
+ * query heads, fp32: 8, share a kv head) are WC_ERR_UNSUPPORTED.
  */
 wc_status wc_cache_attend(const wc_cache* cache, const void* Q, int64_t q_batch, int64_t q_head, const void* k,
                           const void* v, const int32_t* table, const int32_t* lens, int32_t r, const void* Ks,
