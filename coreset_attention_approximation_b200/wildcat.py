@@ -463,9 +463,10 @@ class PagedCache:
         one, with the pages' device current.  The caching allocator is told of
         the tensors' use on a given stream."""
         handle = torch._C._cuda_getCurrentRawStream(self._index)
+        # (the default streams of all devices have one handle, so it alone does not tell whose a stream is)
+        if stream is not None and stream.device != self.device:
+            raise WildcatError(1, f"{what}: the stream is another device's")
         if stream is not None and stream.cuda_stream != handle:
-            if stream.device != self.device:
-                raise WildcatError(1, f"{what}: the stream is another device's")
             for t in tensors + self._kept:
                 if t is not None:
                     t.record_stream(stream)

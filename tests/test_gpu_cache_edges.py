@@ -1,7 +1,8 @@
 """The paged cache on the GPU at its edges: what the calls promise for refused
 sequences, extreme values, other streams and rows outside the cache."""
 
-import numpy as np
+import types
+
 import pytest
 import torch
 
@@ -128,3 +129,22 @@ def test_attend_huge_values(dtype, group, r, room):
     cache_bounds.check(out, ref["out"], ref["out_b"], "out")
     cache_bounds.check(lse, ref["lse"], ref["lse_b"], "lse")
     cache_bounds.check(cache.scores.cpu().double() - case.scores.double(), ref["wts"], ref["wts_b"], "scores")
+
+
+def small_cache(B=2, n_pages=16, hkv=2, page=16, d=64, hq=4):
+    k, v = (torch.randn(n_pages, hkv, page, d, device="cuda").to(BF) for _ in range(2))
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda").reshape(B, -1)
+    scores = torch.rand(B, hkv, table.shape[1] * page, device="cuda")
+    return wildcat.PagedCache(k, v, table, hq=hq, scores=scores)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Also the default stream, whose handle is the same on every device."""
+    cache = small_cache()
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=torch.cuda.default_stream().cuda_stream)
+    K = torch.ones(2, 2, 1, 64, dtype=BF, device="cuda")
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    before = cache.k_pages.clone()
+    with pytest.raises(wildcat.WildcatError, match="another device"):
+        cache.append(K, K, pos, stream=other)
+    assert torch.equal(cache.k_pages, before)
