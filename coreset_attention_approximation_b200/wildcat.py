@@ -420,6 +420,12 @@ class PagedCache:
             raise WildcatError(1, "PagedCache: the pages are on a GPU")
         self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         self.ws[: 256 + 8 * n_pages].zero_()     # the status word and the page counts; the rest is written first
+        # No caller sees the workspace, so none can order its first use on another stream behind these zeros (and
+        # behind whatever used this memory before): they are waited for here, once.  A capture orders its own work.
+        with torch.cuda.device(self.device):
+            made_on = torch.cuda.current_stream()
+            if not torch.cuda.is_current_stream_capturing():
+                made_on.synchronize()
         # what every call passes on, looked up once (a decode step's kernels are as short as the calls that launch them)
         self._shape_ref = ctypes.byref(self.shape)
         self._pools = (k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr())

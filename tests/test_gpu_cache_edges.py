@@ -148,3 +148,23 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(wildcat.WildcatError, match="another device"):
         cache.append(K, K, pos, stream=other)
     assert torch.equal(cache.k_pages, before)
+
+
+def test_first_call_on_another_stream():
+    """Made behind long work on one stream, in memory that was used before,
+    and called at once on another: the workspace is ready."""
+    cache = small_cache()
+    k, v, table, scores = cache.k_pages, cache.v_pages, cache.table, cache.scores
+    lens = torch.tensor([100, 128], dtype=torch.int32, device="cuda")
+    want = cache.evict(lens, 40, into=table, scores_into=torch.zeros_like(scores))["idx"].cpu()
+    n = cache.ws.numel()
+    del cache
+    torch.full((n,), 255, dtype=torch.uint8, device="cuda")       # (freed at once)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                                 # about a tenth of a second
+    cache = wildcat.PagedCache(k, v, table, hq=4, scores=scores)
+    with torch.cuda.stream(side):
+        res = cache.evict(lens, 40)
+    side.synchronize()
+    assert cache.check() == 0 and torch.equal(res["idx"].cpu(), want) and res["lens"].tolist() == [40, 40]
