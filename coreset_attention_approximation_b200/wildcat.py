@@ -426,6 +426,7 @@ class PagedCache:
             made_on = torch.cuda.current_stream()
             if not torch.cuda.is_current_stream_capturing():
                 made_on.synchronize()
+        self._streams = {made_on.cuda_stream}    # that the allocator knows to use the workspace
         # what every call passes on, looked up once (a decode step's kernels are as short as the calls that launch them)
         self._shape_ref = ctypes.byref(self.shape)
         self._pools = (k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr())
@@ -467,7 +468,7 @@ class PagedCache:
     def _launch(self, call, what, stream, args, tensors):
         """call(*args, stream) on the given stream, or the device's current
         one, with the pages' device current.  The caching allocator is told of
-        the tensors' use on a given stream."""
+        the tensors' use on a given stream, and of the workspace's on any."""
         handle = torch._C._cuda_getCurrentRawStream(self._index)
         # (the default streams of all devices have one handle, so it alone does not tell whose a stream is)
         if stream is not None and stream.device != self.device:
@@ -477,6 +478,9 @@ class PagedCache:
                 if t is not None:
                     t.record_stream(stream)
             handle = stream.cuda_stream
+        if handle not in self._streams:          # the workspace outlives the cache until their work is done
+            self.ws.record_stream(stream or torch.cuda.current_stream(self.device))
+            self._streams.add(handle)
         if torch.cuda.current_device() == self._index:
             code = call(*args, handle)
         else:

@@ -168,3 +168,24 @@ def test_first_call_on_another_stream():
         res = cache.evict(lens, 40)
     side.synchronize()
     assert cache.check() == 0 and torch.equal(res["idx"].cpu(), want) and res["lens"].tolist() == [40, 40]
+
+
+def test_the_workspace_outlives_its_cache_on_another_stream():
+    """A cache dropped while another stream still runs its calls: the
+    workspace's memory is not given to anyone before they are done."""
+    cache = small_cache()
+    at = cache.ws.data_ptr()
+    side = torch.cuda.Stream()
+    q = torch.randn(2, 4, 64, device="cuda").to(BF)
+    lens = torch.tensor([100, 128], dtype=torch.int32, device="cuda")
+    cache.attend(q, lens, accumulate=True)                         # (a kernel's first launch may wait for the GPU)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)
+        out = cache.attend(q, lens, accumulate=True)
+    del cache
+    blocks = [x for seg in torch.cuda.memory_snapshot() for x in seg["blocks"] if x["address"] == at]
+    assert not side.query()
+    assert [x["state"] for x in blocks] == ["active_pending_free"]
+    side.synchronize()
+    assert torch.isfinite(out).all()
