@@ -523,7 +523,8 @@ class PagedCache:
     def attend(self, Q, lens, *, coreset=None, accumulate=False, return_lse=False, out=None, stream=None):
         """Attention of one new token per sequence: Q [B, Hq, d] over the first
         lens[b] tokens of sequence b, and over coreset = (Ks, W, rank) beside
-        them (as `weights` and `select` return them; rank None: all r rows).
+        them (as `weights` and `select` return them, with bins or without;
+        rank None: all r rows).
         Returns out [B, Hq, dv] fp32, or (out, lse [B, Hq]).  accumulate: adds
         each key's attention weight, summed over its queries, to `scores`."""
         self._rows(Q, "Q", self._q_shape)
@@ -537,7 +538,13 @@ class PagedCache:
             r = Ks.shape[2] if Ks.dim() == 4 else -1
             self._tensor(Ks, "Ks", (self.batch, self.hkv, r, self.d), self.dtype)
             self._tensor(W, "W", (self.batch, self.hkv, r, self.dv + 1), torch.float32)
-            if rank is not None:
+            if rank is not None and rank.dim() == 3:     # of a binned selection: [B, Hkv, bins]
+                bins = rank.shape[2]
+                self._tensor(rank, "rank", (self.batch, self.hkv, bins), torch.int32)
+                if bins < 1 or r % bins:
+                    raise WildcatError(1, f"PagedCache.attend: {r} coreset rows in {bins} bins")
+                rank = None      # every bin's rows count; those beyond its rank have weight 0 in W
+            elif rank is not None:
                 self._tensor(rank, "rank", (self.batch, self.hkv), torch.int32)
         if out is None:
             out = self._empty(self._o_shape, (self.hq * self.dv, self.dv, 1), torch.float32, stream)

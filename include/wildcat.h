@@ -328,7 +328,8 @@ wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const
  * contiguous, strides in elements) over the first lens[b] tokens of each
  * sequence, and over a coreset where one is given (r > 0: Ks [B, Hkv, r, d],
  * W [B, Hkv, r, dv+1] fp32, both 16-byte aligned, and rank [B, Hkv] as
- * wc_weights leaves them, rank NULL: all r rows): one softmax over both,
+ * wc_weights leaves them; rank NULL: all r rows, as after a selection with bins,
+ * where W is 0 beyond a bin's rank): one softmax over both,
  *   a_i = exp(beta <q, k_i>)  for i < lens[b],   a'_s = exp(beta <q, ks_s>)
  *   L = sum_i a_i + sum_s a'_s W[s, dv]
  *   out[b, g, :] = (sum_i a_i v_i + sum_s a'_s W[s, :dv]) / L,  lse[b, g] = log L

@@ -9,6 +9,7 @@ import torch
 import cache_bounds
 import cache_ref
 from coreset_attention_approximation_b200 import wildcat
+from parity import TOL_OUT, rel_err
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +190,49 @@ def test_the_workspace_outlives_its_cache_on_another_stream():
     assert [x["state"] for x in blocks] == ["active_pending_free"]
     side.synchronize()
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("kw", [{}, {"center": True}, {"bins": 4}, {"bins": 4, "center": True}])
+def test_compressed_prompt_and_exact_tail_are_one_softmax(dtype, kw):
+    """A prompt of 5 distinct keys a bin, which its coreset reproduces exactly,
+    and a tail in the pages: exact attention over all tokens, in value and in
+    normaliser.  The coreset's share is as far off as the library's attention
+    over it alone may be (its tolerance), and the joint row is no further."""
+    B, hq, hkv, n, d, r, tail = 2, 8, 2, 1024, 64, 64, [90, 7]
+    g = torch.Generator().manual_seed(6)
+    distinct = torch.randn(B, hkv, 4, 1, 5, d, generator=g, dtype=torch.float64) * 0.6
+    K = distinct.expand(B, hkv, 4, 52, 5, d).reshape(B, hkv, 4, 260, d)[:, :, :, :256].reshape(B, hkv, n, d).to(dtype)
+    if kw.get("center"):
+        K = (K.double() + 0.4).to(dtype)
+    V = torch.randn(B, hkv, n, d, generator=g, dtype=torch.float64).to(dtype)
+    case = cache_ref.Case(dtype, B, hq, hkv, d, d, 16, 8, tail, seed=9, key_scale=0.6)
+    case.q = (0.6 * case.q.double()).to(dtype)
+    sel = wildcat.select(K.cuda(), r, seed=5, **kw)
+    wts = wildcat.weights(K.cuda(), V.cuda(), sel["piv"], sel["F"], sel["rank"], r, **kw)
+    k, v, table, q, lens, _ = case.on_gpu()
+    cache = wildcat.PagedCache(k, v, table, hq=hq)
+    out, lse = cache.attend(q, lens, coreset=(wts["Ks"], wts["W"], sel["rank"]), return_lse=True)
+    assert cache.check() == 0
+    for b in range(B):
+        for h in range(hkv):
+            kk, vv = case.rows(b, h)
+            kk, vv = torch.cat([K[b, h].double(), kk]), torch.cat([V[b, h].double(), vv])
+            x = case.q[b, 4 * h:4 * h + 4].double() @ kk.T / 8.0
+            want = torch.softmax(x, -1) @ vv
+            assert rel_err(out[b, 4 * h:4 * h + 4].cpu(), want) <= TOL_OUT[dtype]
+            off = (lse[b, 4 * h:4 * h + 4].cpu().double() - torch.logsumexp(x, -1)).abs().max()
+            assert float(off) <= TOL_OUT[dtype]
+
+
+def test_ranks_of_bins_are_checked():
+    cache = small_cache()
+    q = torch.ones(2, 4, 64, dtype=BF, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    Ks, W = torch.ones(2, 2, 8, 64, dtype=BF, device="cuda"), torch.ones(2, 2, 8, 65, device="cuda")
+    for rank in (torch.ones(2, 2, 3), torch.ones(2, 2, 0), torch.ones(2, 1, 4), torch.ones(2, 2, 4).double()):
+        rank = rank.cuda() if rank.dtype == torch.double else rank.to(torch.int32).cuda()
+        with pytest.raises(wildcat.WildcatError):
+            cache.attend(q, lens, coreset=(Ks, W, rank))
+    out = cache.attend(q, lens, coreset=(Ks, W, torch.full((2, 2, 4), 2, dtype=torch.int32, device="cuda")))
+    assert torch.equal(out, torch.ones_like(out))
