@@ -504,7 +504,8 @@ class PagedCache:
         and V [B, Hkv, t, dv] to position pos[b] + j of sequence b; the scores
         there become 0.  pos, count: int32 [B].  K and V may be strided in
         steps of 16 bytes.  Rows beyond the cache's end are not written and
-        reported by `check()`."""
+        reported by `check()`.  Two rows sent to one place (a page that two
+        sequences name) leave pieces of both there."""
         t = K.shape[2] if K.dim() == 4 else -1
         self._rows(K, "K", (self.batch, self.hkv, t, self.d))
         self._rows(V, "V", (self.batch, self.hkv, t, self.dv))

@@ -314,8 +314,10 @@ size_t wc_cache_workspace_bytes(const wc_cache* cache, int32_t accumulate);
  * 16-byte aligned; strides in elements, multiples of 16 bytes) into the pages:
  * row j < count[b] goes to position pos[b] + j (count NULL: all t rows), and
  * scores (if not NULL) become 0 at the positions written.  Nothing else
- * changes; the lengths are the caller's to advance.  t <= 2^30.  Two rows sent
- * to one place leave one of them.
+ * changes; the lengths are the caller's to advance.  t <= 2^30.  A count outside
+ * [0, t] is held to that range.  Rows go to different places: where two are sent
+ * to one (a page that two sequences name, or one twice), the key and the value
+ * there are unspecified, each made of 16-byte pieces of both rows.
  */
 typedef struct { int64_t batch, head, row; } wc_row_strides;
 wc_status wc_cache_append(const wc_cache* cache, int32_t t, const void* K, const wc_row_strides* k_strides,
