@@ -236,3 +236,42 @@ def test_ranks_of_bins_are_checked():
             cache.attend(q, lens, coreset=(Ks, W, rank))
     out = cache.attend(q, lens, coreset=(Ks, W, torch.full((2, 2, 4), 2, dtype=torch.int32, device="cuda")))
     assert torch.equal(out, torch.ones_like(out))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_writes_the_rows_inside_and_no_other(dtype):
+    """Positions and counts outside the cache, a page outside the pool: the
+    rows whose place is inside land there, whole, and everything else (pages,
+    scores) keeps its bits."""
+    B, hkv, page, t, d, dv = 3, 2, 16, 4, 64, 40
+    case = cache_ref.Case(dtype, B, hkv, hkv, d, dv, page, 4, [64] * B, seed=14)
+    k, v, table, _, _, scores = case.on_gpu()
+    cache = wildcat.PagedCache(k, v, table, hq=hkv, scores=scores)
+    bad = case.table.clone()
+    bad[2, 1] = case.n_pages
+    want_k, want_v, want_s = case.k.clone(), case.v.clone(), case.scores.clone()
+    same = lambda x, y: torch.equal(torch.nan_to_num(x.cpu().float(), nan=9e9), torch.nan_to_num(y.float(), nan=9e9))
+    g = torch.Generator().manual_seed(2)
+    for i, (pos, count, tab) in enumerate([
+            ([62, 0, 5], [4, 0, 2], case.table), ([-2, 7, 60], [4, 4, 4], case.table),
+            ([0, 8, 9], [-1, 9, 1], case.table), ([2 ** 31 - 2, 63, -2 ** 31], [4, 1, 4], case.table),
+            ([64, 64, 14], [1, 4, 4], bad), ([20, 21, 30], None, bad), ([-4, -3, 61], None, case.table)]):
+        K = torch.randn(B, hkv, t, d, generator=g).to(dtype)
+        V = torch.randn(B, hkv, t, dv, generator=g).to(dtype)
+        outside = False
+        for b in range(B):
+            n = t if count is None else count[b]
+            outside |= not 0 <= n <= t
+            for j in range(min(max(n, 0), t)):
+                at = pos[b] + j
+                p = int(tab[b, at // page]) if 0 <= at < 64 else -1
+                if not 0 <= p < case.n_pages:
+                    outside = True
+                    continue
+                want_k[p, :, at % page], want_v[p, :, at % page], want_s[b, :, at] = K[b, :, j], V[b, :, j], 0.0
+        cache.table.copy_(tab)
+        cache.append(K.cuda(), V.cuda(), torch.tensor(pos, dtype=torch.int32).cuda(),
+                     None if count is None else torch.tensor(count, dtype=torch.int32).cuda())
+        assert cache.check() == (7 if outside else 0), i
+        assert same(cache.k_pages, want_k) and same(cache.v_pages, want_v), i
+        assert torch.equal(cache.scores.cpu(), want_s), i
