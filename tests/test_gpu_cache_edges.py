@@ -275,3 +275,79 @@ def test_append_writes_the_rows_inside_and_no_other(dtype):
         assert cache.check() == (7 if outside else 0), i
         assert same(cache.k_pages, want_k) and same(cache.v_pages, want_v), i
         assert torch.equal(cache.scores.cpu(), want_s), i
+
+
+def ones_of(case):
+    """The case with every value that is there 1: each output is a row's sum of
+    weights over its normaliser."""
+    case.v = torch.where(torch.isnan(case.v), case.v, torch.ones_like(case.v))
+    return case
+
+
+@ROOM
+@pytest.mark.parametrize("group", [1, 4, 5, 8, 9, 16, 17])
+def test_attend_value_product_keeps_all_bits_of_the_weights(group, room):
+    """bf16 values of 1: out = (sum of the weights' three terms) / (sum of the
+    weights), whatever 2^x rounds to.  Of the numerator, each 16-key product cuts
+    off up to 17 u (u = 2^-24) three times over, at most 3 x 17 u; it and the
+    normaliser each take a rounding for each of at most 19 + 3 additions in a
+    warp, 19 in a join and its factors, and the quotient one: (51 + 2 x 42) u =
+    135 u = 8e-6.  A weight without its third term loses 2^-16 of itself on
+    average (1.5e-5; up to 2^-14), one with another row's terms far more."""
+    case = ones_of(cache_ref.Case(BF, 3, 2 * group, 2, 64, 64, 16, 20 * room, [300, 130, 16], seed=group))
+    k, v, table, q, lens, _ = case.on_gpu()
+    cache = wildcat.PagedCache(k, v, table, hq=2 * group)
+    out = cache.attend(q, lens).cpu().double()
+    assert cache.check() == 0
+    assert float((out - 1).abs().max()) <= 135 * cache_bounds.U
+    # and each column its own: a power of two each, exact in every step
+    scale = (2.0 ** torch.arange(-32, 32).float()).to(BF)
+    cache.v_pages.mul_(scale.cuda())
+    assert torch.equal(cache.attend(q, lens).cpu().double(), out * scale.double())
+
+
+@pytest.mark.parametrize("group", [4, 8, 16])
+def test_attend_does_not_drift_over_long_stretches(group):
+    """512 sequences over the same 65536 keys with values of 1, hundreds of
+    steps a warp: roundings to nearest average out over the rows, so the mean
+    output is 1 up to what each 16-key product cuts off (3 x 17 u at most) and
+    the join's and the quotient's few; sums kept by the tensor core itself would
+    lose part of an u at every step, all one way."""
+    n, B, d = 65536, 512, 16
+    case = ones_of(cache_ref.Case(BF, 1, group, 1, d, d, 4096, 16, [n], seed=group))
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(B, group, d, generator=g).to(BF).cuda()
+    table = case.table.cuda().expand(B, -1).contiguous()
+    cache = wildcat.PagedCache(case.k.cuda(), case.v.cuda(), table, hq=group)
+    out = cache.attend(q, torch.full((B,), n, dtype=torch.int32, device="cuda")).double()
+    assert cache.check() == 0
+    assert abs(float(out.mean()) - 1) <= (51 + 9) * cache_bounds.U
+    # one row: 2 x 900 steps' roundings of random signs, of which the largest of a few thousand is 5 deviations
+    # of sqrt(1800 / 3) u each, beside the 60 u
+    assert float((out - 1).abs().max()) <= (60 + 5 * (1800 / 3) ** 0.5) * cache_bounds.U
+
+
+@ROOM
+@pytest.mark.parametrize("dtype,hq,hkv,d,dv,page,tf", [
+    (BF, 8, 2, 128, 128, 16, False), (BF, 32, 4, 128, 128, 64, True), (BF, 16, 1, 128, 64, 32, False),
+    (BF, 10, 2, 96, 96, 24, False), (BF, 24, 2, 256, 256, 7, True), (BF, 36, 1, 64, 128, 16, False),
+    (F32, 8, 2, 64, 64, 16, False), (F32, 16, 1, 256, 256, 32, False), (F32, 20, 2, 40, 136, 16, False)])
+@pytest.mark.parametrize("core", [0, 1, 70])
+def test_attend_every_value_within_its_own_bound(dtype, hq, hkv, d, dv, page, tf, core, room):
+    lens = [0, 1, 16, 65, 300]
+    case = cache_ref.Case(dtype, len(lens), hq, hkv, d, dv, page, -(-304 * room // page), lens, tokens_first=tf, seed=d + core)
+    cs = None
+    if core:
+        g = torch.Generator().manual_seed(core)
+        w = torch.exp(torch.randn(case.B, hkv, core, 1, generator=g))
+        cs = (torch.randn(case.B, hkv, core, d, generator=g).to(dtype),
+              torch.cat([w * torch.randn(case.B, hkv, core, dv, generator=g), w], -1),
+              torch.randint(0, core + 1, (case.B, hkv), generator=g).to(torch.int32))
+    k, v, table, q, lens, scores = case.on_gpu()
+    cache = wildcat.PagedCache(k, v, table, hq=hq, scores=scores)
+    out, lse = cache.attend(q, lens, coreset=cs and tuple(x.cuda() for x in cs), accumulate=True, return_lse=True)
+    assert cache.check() == 0
+    ref = cache_bounds.attend(case, cs)
+    cache_bounds.check(out, ref["out"], ref["out_b"], "out")
+    cache_bounds.check(lse, ref["lse"], ref["lse_b"], "lse")
+    cache_bounds.check(cache.scores.cpu().double() - case.scores.double(), ref["wts"], ref["wts_b"], "scores")
