@@ -1,6 +1,7 @@
 """The paged cache on the GPU at its edges: what the calls promise for refused
 sequences, extreme values, other streams and rows outside the cache."""
 
+import math
 import types
 
 import pytest
@@ -292,8 +293,7 @@ def test_attend_value_product_keeps_all_bits_of_the_weights(group, room):
     off up to 17 u (u = 2^-24) three times over, at most 3 x 17 u; it and the
     normaliser each take a rounding for each of at most 19 + 3 additions in a
     warp, 19 in a join and its factors, and the quotient one: (51 + 2 x 42) u =
-    135 u = 8e-6.  A weight without its third term loses 2^-16 of itself on
-    average (1.5e-5; up to 2^-14), one with another row's terms far more."""
+    135 u = 8e-6.  A second term is some thousandths of its weight."""
     case = ones_of(cache_ref.Case(BF, 3, 2 * group, 2, 64, 64, 16, 20 * room, [300, 130, 16], seed=group))
     k, v, table, q, lens, _ = case.on_gpu()
     cache = wildcat.PagedCache(k, v, table, hq=2 * group)
@@ -304,6 +304,33 @@ def test_attend_value_product_keeps_all_bits_of_the_weights(group, room):
     scale = (2.0 ** torch.arange(-32, 32).float()).to(BF)
     cache.v_pages.mul_(scale.cuda())
     assert torch.equal(cache.attend(q, lens).cpu().double(), out * scale.double())
+
+
+@ROOM
+@pytest.mark.parametrize("group", [1, 2, 4, 7, 8, 13, 16])
+def test_attend_value_product_keeps_the_last_bits_of_the_weights(group, room):
+    """The same with one key of logit 0 and all others of a logit whose weight
+    beside it is t / 2, t = 1 + 2^-8 + 200 2^-23: its third term is 200 2^-23 (a
+    few units more or less, as 2^x and the scale round), 2.4e-5 of it and three
+    times the bound.  Every second query row is 0: weights of exactly 2^-8, whose
+    second and third terms are nothing, so another row's terms would show too."""
+    t = 1 + 2.0 ** -8 + 200 * 2.0 ** -23
+    case = ones_of(cache_ref.Case(BF, 2, group, 1, 64, 64, 16, 20 * room, [300, 40], seed=group))
+    live = ~torch.isnan(case.k)
+    case.k = torch.where(live, torch.zeros_like(case.k), case.k)
+    case.k[..., 0] = torch.where(live[..., 0], -torch.ones_like(case.k[..., 0]), case.k[..., 0])
+    for b in range(2):
+        case.k[int(case.table[b, 0]), 0, 0, 0] = 0
+    case.q.zero_()
+    case.q[:, ::2, 0] = 1
+    k, v, table, q, lens, _ = case.on_gpu()
+    cache = wildcat.PagedCache(k, v, table, hq=group, scale=math.log(2.0) * (1 - math.log2(t)))
+    out, lse = cache.attend(q, lens, return_lse=True)
+    assert cache.check() == 0
+    n = case.lens.double()[:, None]
+    want = torch.log(torch.where(torch.arange(group) % 2 == 0, 1 + (n - 1) * t / 2, n))
+    assert float((lse.cpu().double() - want).abs().max()) <= 64 * cache_bounds.U      # the case is the one meant
+    assert float((out.cpu().double() - 1).abs().max()) <= 135 * cache_bounds.U
 
 
 @pytest.mark.parametrize("group", [4, 8, 16])
