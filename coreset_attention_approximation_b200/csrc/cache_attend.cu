@@ -8,8 +8,9 @@
 // The key tiles of the whole batch are divided over the warps (Share in
 // wc_cache.cuh), whatever the lengths; a warp streams its tiles through a ring
 // of its own in shared memory, on from one sequence or head to the next, and
-// never waits for another.  The coreset is a kernel of its own that runs beside
-// it.  A last kernel joins the partial rows, in order of the stretches and of
+// never waits for another.  The coreset is a kernel of its own ahead of it, whose
+// blocks and the pages' do not fit an SM together: a pages' block starts as the
+// coreset's blocks leave.  A last kernel joins the partial rows, in order of the stretches and of
 // the coreset's splits.
 //
 // The kernels overlap by programmatic dependent launch: each may start before
@@ -446,8 +447,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 // 1.3 times as long over all), the last few values one by one.  A lane holds
 // columns lane, lane + 32, ... and the row's last value is its weight in the
 // normaliser.  The logits of bf16 keys on tensor cores, the sums in fp32 on
-// CUDA cores: W's values cancel one another.  Bound by the issue of those sums
-// and of the copies (8 x 1024 rows of 8 heads in about 14 us, 3.5 TB/s).
+// CUDA cores: W's values cancel one another.  8 x 1024 rows of 8 heads take 16.9 us
+// (cold, 3.0 TB/s): each warp has only four steps of 720 instructions, and with
+// 3.3 warps a scheduler (96 registers, 52 KB of stages a block) the latencies of a
+// step's loads, shuffles and sums are not covered (a scheduler issues in half of
+// its active cycles).
 template <typename T, int RG, int NT, int DP>
 __global__ void __launch_bounds__(kCoresetWarps * 32) cache_coreset_kernel(const AttendArgs a) {
     constexpr int WARPS = kCoresetWarps, COLS = DP / 32;
@@ -674,7 +678,11 @@ __device__ void finish_unit(const AttendArgs& a, const Walk& u, int64_t row0, in
 // fp32 pages, on CUDA cores (their products keep 24 bits): 8 keys a step, two or
 // three stages a warp.  For the logits a lane holds one key and a quarter of the
 // width, for the values four columns (and, where fewer than 32 lanes cover the
-// width, every second key).  DP: d and dv rounded up to 64, 128 or 256.
+// width, every second key).  DP: d and dv rounded up to 64, 128 or 256.  Long
+// passes are bound by bytes (4 x 32768 tokens of 128-wide heads: 169 us, 6.35 TB/s).
+// Few bytes a warp are not: 57 MB of ragged 64-wide heads take 16.8 us (3.3 TB/s),
+// where a step moves 4 KB behind a chain of shuffles, 2^x and shared memory, 400
+// instructions, and a scheduler issues in 39 % of its cycles.
 constexpr int kSimtKeys = 8;
 template <int DP> constexpr int kSimtStages = DP > 64 ? 2 : 3;
 
@@ -898,6 +906,8 @@ template <int DP> using MmaRing = Ring<kMmaKeys, DP, 2, kMmaStages<DP>>;
 //      the copies carry the terms, so one product adds all three
 //   2  up to 8 rows, each twice: two products
 //   3  up to 16 rows: three products
+// DP = 256 needs more than the 255 registers there are and spills up to 628 bytes
+// a thread: 2 x 32768 tokens 106 us, 5.0 TB/s (128-wide heads of as many bytes 92 us).
 // SHORT: as above.
 template <int DP, int SETS, bool SHORT>
 __global__ void __launch_bounds__(kMmaWarps<DP> * 32) cache_attend_mma_kernel(const AttendArgs a) {

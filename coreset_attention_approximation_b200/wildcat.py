@@ -374,7 +374,8 @@ class PagedCache:
     [B, max_pages] int32 (contiguous): token t of sequence b is in slot
     t % page of page table[b, t // page].  hq: query heads.  scores
     [B, Hkv, max_pages * page] fp32 (contiguous): accumulated attention
-    weights, needed to accumulate and to evict.
+    weights, needed to accumulate and to evict; a cache with scores keeps
+    4 B hq max_pages page bytes of workspace for a step's logits as well.
 
     Lengths, positions and counts are int32 CUDA tensors that the caller keeps
     and advances, so a captured graph serves a growing cache.  The tensors
